@@ -230,8 +230,8 @@ def _plans(s):
         s["values"] = ctx.state8_plan(parts("m_out") + parts("v_out"), parts("m_code") + parts("v_code"),
                                       scales("m_scale") + scales("v_scale"))
     if op in ("adamw32", "adamw8"):
-        from matrix_aware_optimizer_step_b200 import adamw_plan_hparams
-        s["hp"] = adamw_plan_hparams(lr=LR, beta1=BETA1, beta2=case["beta2"], eps=EPS, weight_decay=DECAY)
+        from matrix_aware_optimizer_step_b200 import default_adamw_plan_hparams
+        s["hp"] = default_adamw_plan_hparams(lr=LR, beta1=BETA1, beta2=case["beta2"], eps=EPS, weight_decay=DECAY)
 
 
 # ---------------------------------------------------------------------------
