@@ -176,6 +176,63 @@ typedef struct {
 
 typedef struct muon_ctx muon_ctx;
 
+/* One tensor of an AdamW plan (muon_adamw_plan_create); all of param, grad,
+ * exp_avg, exp_avg_sq and param_copy have numel elements and need only the
+ * alignment of one element (16 bytes, 8 for 8-bit moments, for full speed).
+ *   param        fp32 or bf16 (param_dtype), updated in place.
+ *   grad         fp32 or bf16 (grad_dtype), read only; rebound by
+ *                muon_plan_bind_grads.
+ *   exp_avg, exp_avg_sq  32-bit plans: fp32.  8-bit plans: int8 and uint8
+ *                codes.
+ *   exp_avg_scale, exp_avg_sq_scale  8-bit plans: one fp32 for each 256
+ *                consecutive elements, ceil(numel / 256) in all; NULL in
+ *                32-bit plans.  A code c stands for m = c |c| scale and
+ *                sqrt(v) = (c + 1)^2 scale: all-zero codes with zero scales
+ *                are zero moments.
+ *   param_copy   optional (NULL = off), with an fp32 param: receives the new
+ *                parameter rounded to bf16. */
+typedef struct {
+  int64_t numel;
+  int32_t param_dtype;             /* muon_dtype */
+  int32_t grad_dtype;              /* muon_dtype */
+  void* param;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale;
+  float* exp_avg_sq_scale;
+  void* param_copy;
+} muon_plan_tensor;
+
+/* Hyper-parameters of a plan's AdamW step, in 64 bits: 1 - beta2 of 0.999
+ * formed from a 32-bit beta2 is off by 5e-5. */
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+} muon_adamw_plan_hparams;
+
+/* One gradient of a norm plan. */
+typedef struct {
+  int64_t numel;
+  int32_t grad_dtype;              /* muon_dtype */
+  int32_t reserved;
+  const void* grad;
+} muon_grad_tensor;
+
+/* One moment tensor of a conversion plan: numel values (fp32 or bf16), its
+ * codes (int8 first moments, uint8 second moments) and ceil(numel / 256)
+ * scales, the form of muon_plan_tensor. */
+typedef struct {
+  int64_t numel;
+  int32_t value_dtype;             /* muon_dtype */
+  int32_t second_moment;           /* 0: exp_avg, 1: exp_avg_sq */
+  void* values;
+  void* codes;
+  float* scales;
+} muon_state8_tensor;
+
+/* A list of tensors laid out once, for calls that repeat every step. */
+typedef struct muon_plan muon_plan;
+
 /* Source: "Muon: An optimizer for the hidden layers of neural networks",
  * sections "Usage" and "Hyperparameter tuning" (lr 0.02, momentum 0.95,
  * weight decay 0.01, Nesterov, 5 steps); "Muon: when the LLM optimizer
@@ -268,6 +325,105 @@ MUON_API muon_status muon_orthogonalize(muon_ctx* ctx, const muon_ns_group* grou
  * launch. */
 MUON_API muon_status muon_adamw_step(muon_ctx* ctx, const muon_adamw_tensor* tensors, int32_t n,
                             const muon_adamw_hparams* hp, int64_t step, void* stream);
+
+/* Source: "Muon: An optimizer for the hidden layers of neural networks",
+ * section "Usage" (the AdamW defaults of muon_default_adamw_hparams, in 64
+ * bits).  hp NULL: no effect. */
+MUON_API void muon_default_adamw_plan_hparams(muon_adamw_plan_hparams* hp);
+
+/* No counterpart on the pages (the step itself: muon_adamw_plan_step).
+ * Lay out n tensors for AdamW steps with moments of state_bits (32 or 8)
+ * bits.  The plan keeps the tensors' addresses, not the tensors: the caller
+ * keeps them alive and in place until the plan is destroyed.  No tensor that
+ * a step writes may overlap another tensor of the plan.  Tensors of numel 0
+ * are allowed.  Allocates the plan's table and synchronises with its upload;
+ * not to be called during a stream capture.  *plan is NULL on failure.
+ * Errors: bad lists, types, overlaps or pointers -> MUON_ERR_INVALID_ARG. */
+MUON_API muon_status muon_adamw_plan_create(muon_ctx* ctx, const muon_plan_tensor* tensors, int32_t n,
+                                            int32_t state_bits, muon_plan** plan);
+
+/* Source: "Muon: An optimizer for the hidden layers of neural networks",
+ * section "Usage" (every parameter that is not a hidden 2-D weight goes to
+ * AdamW); "Muon: when the LLM optimizer treats weight matrices as
+ * matrices", section 1 (the first and second moments).
+ * One bias-corrected AdamW step with decoupled weight decay over the plan's
+ * tensors.  Moments and parameter are computed in fp32 from the unrounded
+ * new moments; only what is stored is rounded.
+ *   step        counts from 1.
+ *   step_ptr    optional device int64 (8-byte aligned) read by the kernels
+ *               instead of step, for steps captured into a CUDA graph; when
+ *               it holds less than 1 the step writes nothing.
+ *   lr_ptr      optional device float read instead of hp->lr; when it is not
+ *               finite the step writes nothing.
+ *   grad_scale  optional device float that multiplies every gradient (the
+ *               factor of muon_grad_norm_run); when it is not finite the step
+ *               writes nothing.
+ *   stochastic  0: codes and bf16 parameters are rounded to nearest.  Else
+ *               they are rounded up with the probability of what is dropped,
+ *               by numbers hashed from (seed, step, the tensor's place in the
+ *               plan, the element): the same arguments give the same result.
+ *               param_copy is always rounded to nearest.
+ * 8-bit moments: a block of 256 elements holding a non-finite moment is
+ * stored as NaN throughout; one whose largest moment is below 2^-100 as
+ * zero.  The call only launches kernels, so it can be captured; calls on the
+ * same tensors must be ordered.  Errors: step < 1 without step_ptr, betas
+ * outside [0, 1), eps that is not > 0 in fp32, non-finite values, misaligned
+ * device scalars, a plan of another kind or of a destroyed context ->
+ * MUON_ERR_INVALID_ARG, before any launch. */
+MUON_API muon_status muon_adamw_plan_step(muon_plan* plan, const muon_adamw_plan_hparams* hp, int64_t step,
+                                          const int64_t* step_ptr, const float* lr_ptr, const float* grad_scale,
+                                          int32_t stochastic, uint32_t seed, void* stream);
+
+/* No counterpart on the pages (gradient clipping is the caller's).
+ * Lay out n gradients for muon_grad_norm_run; conditions as
+ * muon_adamw_plan_create, except that gradients may overlap. */
+MUON_API muon_status muon_grad_norm_plan_create(muon_ctx* ctx, const muon_grad_tensor* tensors, int32_t n,
+                                                muon_plan** plan);
+
+/* No counterpart on the pages (memory planning).  Bytes of the output buffer
+ * of muon_grad_norm_run, written to *bytes; host only. */
+MUON_API muon_status muon_grad_norm_out_bytes(const muon_plan* plan, size_t* bytes);
+
+/* No counterpart on the pages (gradient clipping is the caller's).
+ * out[0] = norm = sqrt(sum of squares over every gradient of the plan),
+ * out[1] = min(1, max_norm / (norm + 1e-6)), or NaN when the norm is not
+ * finite.  max_norm >= 0, infinity to measure only.  Squares are summed in
+ * fp32 within 8 elements (in 64 bits where that would leave fp32's range)
+ * and in 64 bits beyond, in a fixed order: the same gradients give the same
+ * bits.  out is a 16-byte aligned device buffer of muon_grad_norm_out_bytes;
+ * behind its two results it holds the call's workspace, zeroed by the caller
+ * before the buffer's first use.  Runs that may overlap in time need buffers
+ * of their own.  The call only launches kernels.  A raised device flag does
+ * not stop it.  Errors -> MUON_ERR_INVALID_ARG, before any launch. */
+MUON_API muon_status muon_grad_norm_run(muon_plan* plan, double max_norm, float* out, void* stream);
+
+/* No counterpart on the pages (resource management).  Replace the gradients
+ * of an AdamW or norm plan by n others of the same sizes and types, in list
+ * order; host only.  Later calls use them; launched, captured and replayed
+ * ones keep what they were launched with. */
+MUON_API muon_status muon_plan_bind_grads(muon_plan* plan, const void* const* grads, int32_t n);
+
+/* No counterpart on the pages (8-bit moments).  Lay out n moment tensors for
+ * conversion between values and the 8-bit form; no two may overlap.
+ * Conditions as muon_adamw_plan_create. */
+MUON_API muon_status muon_state8_plan_create(muon_ctx* ctx, const muon_state8_tensor* tensors, int32_t n,
+                                             muon_plan** plan);
+
+/* No counterpart on the pages (8-bit moments).  Values -> codes and scales,
+ * rounded to nearest; blocks as in muon_adamw_plan_step.  A negative second
+ * moment makes its block NaN. */
+MUON_API muon_status muon_state8_pack(muon_plan* plan, void* stream);
+
+/* No counterpart on the pages (8-bit moments).  Codes and scales -> the
+ * values they stand for, in fp32, rounded once to bf16 where the values are
+ * bf16. */
+MUON_API muon_status muon_state8_unpack(muon_plan* plan, void* stream);
+
+/* No counterpart on the pages (resource management).  Free a plan of any
+ * kind (synchronises the device).  Graphs that captured its calls must not
+ * be replayed afterwards.  Plans outlive their context only to be destroyed:
+ * other calls on them then return MUON_ERR_INVALID_ARG.  NULL: no effect. */
+MUON_API void muon_plan_destroy(muon_plan* plan);
 
 /* Source: "The Newton-Muon Optimizer", section "What Is Newton-Muon?" (the
  * refresh half of the refresh/apply step: the activation second moment,

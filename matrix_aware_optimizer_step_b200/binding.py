@@ -37,6 +37,9 @@ EXPORTED = [
     "muon_check_device", "muon_selftest_wait", "muon_selftest_gemm", "muon_launch_count", "muon_profile_enable",
     "muon_profile_read",
     "muon_orthogonalize_noalloc", "muon_partition",
+    "muon_default_adamw_plan_hparams", "muon_adamw_plan_create", "muon_adamw_plan_step",
+    "muon_grad_norm_plan_create", "muon_grad_norm_out_bytes", "muon_grad_norm_run", "muon_plan_bind_grads",
+    "muon_state8_plan_create", "muon_state8_pack", "muon_state8_unpack", "muon_plan_destroy",
 ]
 
 KERNEL_KINDS = ["momentum", "gram", "poly", "update", "apply", "adamw", "newton_refresh",
@@ -91,6 +94,30 @@ class ActDesc(ctypes.Structure):
                 ("s_inv_split", ctypes.c_void_p)]
 
 
+class PlanTensor(ctypes.Structure):
+    _fields_ = [("numel", ctypes.c_int64), ("param_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("param", ctypes.c_void_p),
+                ("grad", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
+                ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+                ("exp_avg_sq_scale", ctypes.c_void_p), ("param_copy", ctypes.c_void_p)]
+
+
+class AdamwPlanHparams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double)]
+
+
+class GradTensor(ctypes.Structure):
+    _fields_ = [("numel", ctypes.c_int64), ("grad_dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("grad", ctypes.c_void_p)]
+
+
+class State8Tensor(ctypes.Structure):
+    _fields_ = [("numel", ctypes.c_int64), ("value_dtype", ctypes.c_int32),
+                ("second_moment", ctypes.c_int32), ("values", ctypes.c_void_p),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
 class KernelTimes(ctypes.Structure):
     _fields_ = [("ms", ctypes.c_double * len(KERNEL_KINDS)), ("launches", ctypes.c_uint64 * len(KERNEL_KINDS))]
 
@@ -131,6 +158,18 @@ def load_library() -> ctypes.CDLL:
         "muon_profile_enable": (st, [vp, ctypes.c_int]),
         "muon_profile_read": (st, [vp, ctypes.POINTER(KernelTimes)]),
         "muon_orthogonalize_noalloc": (st, [vp, i32, i64, i64, vp, ctypes.POINTER(Hparams), vp]),
+        "muon_default_adamw_plan_hparams": (None, [ctypes.POINTER(AdamwPlanHparams)]),
+        "muon_adamw_plan_create": (st, [vp, ctypes.POINTER(PlanTensor), i32, i32, ctypes.POINTER(vp)]),
+        "muon_adamw_plan_step": (st, [vp, ctypes.POINTER(AdamwPlanHparams), i64, vp, vp, vp, i32,
+                                      ctypes.c_uint32, vp]),
+        "muon_grad_norm_plan_create": (st, [vp, ctypes.POINTER(GradTensor), i32, ctypes.POINTER(vp)]),
+        "muon_grad_norm_out_bytes": (st, [vp, ctypes.POINTER(sz)]),
+        "muon_grad_norm_run": (st, [vp, ctypes.c_double, vp, vp]),
+        "muon_plan_bind_grads": (st, [vp, vp, i32]),
+        "muon_state8_plan_create": (st, [vp, ctypes.POINTER(State8Tensor), i32, ctypes.POINTER(vp)]),
+        "muon_state8_pack": (st, [vp, vp]),
+        "muon_state8_unpack": (st, [vp, vp]),
+        "muon_plan_destroy": (None, [vp]),
         "muon_partition": (st, [ctypes.POINTER(i64), ctypes.POINTER(i64), i32, i32,
                                 ctypes.POINTER(i32)]),
     }
@@ -158,6 +197,16 @@ def default_adamw_hparams(**over) -> AdamwHparams:
     hp = AdamwHparams()
     load_library().muon_default_adamw_hparams(ctypes.byref(hp))
     for k, v in over.items():
+        setattr(hp, k, v)
+    return hp
+
+
+def default_adamw_plan_hparams(**over) -> AdamwPlanHparams:
+    hp = AdamwPlanHparams()
+    load_library().muon_default_adamw_plan_hparams(ctypes.byref(hp))
+    for k, v in over.items():
+        if k not in dict(AdamwPlanHparams._fields_):
+            raise TypeError(f"unknown hyper-parameter {k}")
         setattr(hp, k, v)
     return hp
 
@@ -368,6 +417,28 @@ class MuonContext:
             arr[i].exp_avg_sq = exp_avg_sqs[i].data_ptr()
         self._check(self._lib.muon_adamw_step(self._ctx, arr, n, ctypes.byref(hp), int(step),
                                               _stream_ptr(stream)), "muon_adamw_step")
+
+    def adamw_plan(self, params: Sequence, grads: Sequence, exp_avgs: Sequence, exp_avg_sqs: Sequence,
+                   exp_avg_scales: Optional[Sequence] = None, exp_avg_sq_scales: Optional[Sequence] = None,
+                   param_copies: Optional[Sequence] = None):
+        """An AdamwPlan over these tensors (lists of one length): fp32 or bf16
+        params and grads; moments fp32, or, with both lists of scales, 8-bit
+        (int8 exp_avgs, uint8 exp_avg_sqs).  param_copies[i] (bf16, or None)
+        receives the new fp32 params[i] rounded to bf16."""
+        from .plans import AdamwPlan
+        return AdamwPlan(self, params, grads, exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales, param_copies)
+
+    def grad_norm_plan(self, grads: Sequence):
+        """A GradNormPlan over these gradients (fp32 or bf16)."""
+        from .plans import GradNormPlan
+        return GradNormPlan(self, grads)
+
+    def state8_plan(self, values: Sequence, codes: Sequence, scales: Sequence):
+        """A State8Plan that converts values[i] (fp32 or bf16 moments) to and
+        from codes[i] (int8: a first moment, uint8: a second moment) with
+        scales[i] (fp32, one per 256 elements)."""
+        from .plans import State8Plan
+        return State8Plan(self, values, codes, scales)
 
     def newton_refresh(self, acts: Sequence, s_invs: Sequence, nblocks: Sequence[int],
                        damping: float = 0.0, stream=None, splits: Optional[Sequence] = None):

@@ -29,8 +29,11 @@
 #include "newton.cuh"
 #include "ns_gemm.cuh"
 #include "small_ns.cuh"
+#include "state_ops.cuh"
 
 using namespace muon;
+
+struct muon_plan;
 
 struct muon_ctx {
   int device = 0;
@@ -49,6 +52,7 @@ struct muon_ctx {
   uint64_t launches = 0;
   cudaStream_t last_stream = nullptr;
   std::string err;
+  std::vector<muon_plan*> plans;   // orphaned when the context goes
   // profiler: event pairs per kernel class, recycled through a pool
   bool prof = false;
   std::vector<std::pair<cudaEvent_t, cudaEvent_t>> prof_pending[MUON_K_COUNT];
@@ -1393,6 +1397,8 @@ __global__ void noalloc_poison_kernel(const int* flags, float* out, int64_t n) {
     out[i] = nan;
 }
 
+#include "state_plans.cuh"
+
 extern "C" {
 
 void muon_default_hparams(muon_hparams* hp) {
@@ -1475,6 +1481,7 @@ void muon_destroy(muon_ctx* ctx) {
       cudaEventDestroy(pr.second);
     }
   for (auto e : ctx->prof_pool) cudaEventDestroy(e);
+  for (muon_plan* p : ctx->plans) p->ctx = nullptr;
   delete ctx;
 }
 

@@ -177,6 +177,47 @@ def adamw_step(param, grad, exp_avg, exp_avg_sq, step, hp=None):
 
 
 # ---------------------------------------------------------------------------
+# Moments in 8 bits, gradient norm
+# ---------------------------------------------------------------------------
+
+STATE8_BLOCK = 256
+
+
+def state8_encode(x, second_moment=False, u=0.5):
+    """(codes, scales, real-valued codes) of a 1-D moment tensor, one scale
+    per 256 elements.  First moments: m = c |c| s with s = max|m| / 127^2.
+    Second moments: sqrt(v) = (c + 1)^2 s with s = max sqrt(v) / 256^2.  A
+    code is floor(y + u) of the real-valued code y."""
+    x = np.asarray(x, dtype=np.float64).ravel()
+    levels = 256.0 if second_moment else 127.0
+    mag = np.sqrt(x) if second_moment else np.abs(x)
+    codes, ys, scales = np.zeros(x.size), np.zeros(x.size), []
+    u = np.broadcast_to(np.asarray(u, dtype=np.float64), x.shape)
+    for at in range(0, x.size, STATE8_BLOCK):
+        b = slice(at, min(x.size, at + STATE8_BLOCK))
+        big = mag[b].max()
+        scales.append(big / levels ** 2)
+        if big > 0:
+            ys[b] = levels * np.sqrt(mag[b] / big)
+            c = np.minimum(np.floor(ys[b] + u[b]), levels)
+            codes[b] = np.maximum(c, 1.0) - 1.0 if second_moment else np.sign(x[b]) * c
+    return codes, np.array(scales), ys
+
+
+def state8_decode(codes, scales, second_moment=False):
+    """The moments that codes and scales stand for."""
+    c = np.asarray(codes, dtype=np.float64).ravel()
+    s = np.repeat(np.asarray(scales, dtype=np.float64), STATE8_BLOCK)[:c.size]
+    return ((c + 1.0) ** 2 * s) ** 2 if second_moment else c * np.abs(c) * s
+
+
+def grad_norm(grads, max_norm=math.inf):
+    """(2-norm over all gradients, factor that clips it to max_norm)."""
+    norm = math.sqrt(sum(float(np.sum(np.asarray(g, dtype=np.float64) ** 2)) for g in grads))
+    return norm, min(1.0, max_norm / (norm + 1e-6))
+
+
+# ---------------------------------------------------------------------------
 # Newton-Muon
 # ---------------------------------------------------------------------------
 
