@@ -43,7 +43,7 @@ namespace muon {
 
 constexpr int ST_THREADS = 256;
 constexpr int Q_BLOCK = 256;            // elements that share a scale: one warp, 8 per lane
-constexpr int ST_CHUNK = 4096;          // elements of one thread block (two per warp and pass)
+constexpr int ST_CHUNK = 2048;          // elements of one thread block: a block of 256 for each warp
 constexpr int MAX_SLOTS = 480;          // tensors of one launch: their gradient pointers are a kernel
                                         // parameter (3840 B), so rebinding gradients touches no
                                         // device memory that a launch in flight could be reading
@@ -77,6 +77,7 @@ struct AdamPlanScalars {
   const float* lr_ptr;
   const float* grad_scale;
   uint32_t seed_key, step;                    // mixed seed, low bits of the step
+  float minus_zero;                           // -0 (adam_moments8)
 };
 
 // 32-bit mixer: xor-shifts and odd multiplications, each a bijection.
@@ -217,17 +218,222 @@ __device__ __forceinline__ uint32_t encode_r(float r, float inv, float u) {
   return static_cast<uint32_t>(fminf(fmaxf(real_code(r, inv, u), 1.f), 256.f)) - 1u;
 }
 
-// New moments, each operation rounded once.
-__device__ __forceinline__ void adam_moments(float& m, float& v, float g, const AdamPlanScalars& s) {
-  m = __fadd_rn(__fmul_rn(m, s.beta1), __fmul_rn(g, s.one_beta1));
-  v = __fadd_rn(__fmul_rn(v, s.beta2), __fmul_rn(__fmul_rn(g, g), s.one_beta2));
+// ---------------------------------------------------------------------------
+// the same codes at streaming speed
+// ---------------------------------------------------------------------------
+// IEEE square roots and integer conversions for two codes an element made the
+// 8-bit step compute bound.  The fast path forms y with sqrt.approx (relative
+// error at most 2^-23) and rounds by adding 1.5 * 2^23; where y + u lies so
+// near an integer that this could round to another code than the definition
+// (FAR_* below, both sides' errors added up), the code is formed again by the
+// definition.  A 16-bit u enters as h / 2^16 - 1/2, short of its 2^-17.
+//
+// Errors in y, in units of 2^-23 relative unless absolute:
+//   m: sqrt.approx 1, IEEE root 1/2; times 127: 2.3e-5.  y + u: 2^-17 on the
+//      definition's side, 2^-18 here, 2^-17 for the missing part of u: 1.9e-5.
+//   r: r itself 1 + 1/2, r * inv twice 1/2, halved by the root: 1.25; the root
+//      1 + 1/2; times 256: 8.4e-5.  y + u: 2^-17 + 2^-17 + 2^-17: 2.3e-5
+//      (2^-16 each above 256 only where min() decides).
+constexpr float FAR_M = 0.5f - 6.1e-5f;
+constexpr float FAR_R = 0.5f - 1.9e-4f;
+constexpr float ROUND_MAGIC = 12582912.f;   // 1.5 * 2^23
+
+__device__ __forceinline__ float sqrt_fast(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// max(a, |b|, |c|), NaN if any is
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float y;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+__device__ __forceinline__ float max_abs8(const float (&x)[8]) {
+  return max_abs3(max_abs3(max_abs3(max_abs3(0.f, x[0], x[1]), x[2], x[3]), x[4], x[5]), x[6], x[7]);
+}
+
+// Two fp32 values in a register pair: sm_100a rounds both halves of a packed
+// operation as the scalar one would, at one issue slot for two elements.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 pack2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(F2 a, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v)); }
+__device__ __forceinline__ F2 both(float x) { return pack2(x, x); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// byte k of w as the low mantissa byte of 2^23: 2^23 + byte
+__device__ __forceinline__ float magic_byte(uint32_t w, int k) {
+  return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7650 | k));
+}
+
+// h / 2^16 - 1/2 of the low (or high) half of w, its bytes swapped for `swap`
+__device__ __forceinline__ float half_unit(uint32_t w, int high, bool swap) {
+  const int b0 = 2 * high + (swap ? 1 : 0), b1 = 2 * high + (swap ? 0 : 1);
+  return fmaf(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7600 | (b1 << 4) | b0)), 1.f / 65536.f, -128.5f);
+}
+
+__device__ __forceinline__ uint32_t pack_low_bytes(const float (&z)[8], int at) {
+  const uint32_t a = __byte_perm(__float_as_uint(z[at]), __float_as_uint(z[at + 1]), 0x0040);
+  const uint32_t b = __byte_perm(__float_as_uint(z[at + 2]), __float_as_uint(z[at + 3]), 0x0040);
+  return __byte_perm(a, b, 0x5410);
+}
+
+// The block's real-valued codes a[k], moved by u - 1/2, rounded to nearest:
+// low mantissa bytes of z[k] hold the codes, and the return value says whether
+// any lies within the limits of a boundary.
+template <bool SECOND, bool STOCH>
+__device__ __forceinline__ bool round8(const float (&x)[8], float inv, const uint32_t (&h)[4], float (&a)[8], float (&z)[8]) {
+  constexpr float MAGIC = SECOND ? ROUND_MAGIC - 1.f : ROUND_MAGIC;
+  const F2 i2 = both(inv), up = both(MAGIC), down = both(-MAGIC), minus = both(-1.f);
+  float f[8];
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) {
+    float lo, hi;
+    unpack2(mul2(pack2(x[k], x[k + 1]), i2), lo, hi);
+    lo = sqrt_fast(fabsf(lo));
+    hi = sqrt_fast(fabsf(hi));
+    if (STOCH) {
+      lo += half_unit(h[k >> 1], 0, !SECOND);
+      hi += half_unit(h[k >> 1], 1, !SECOND);
+    }
+    a[k] = SECOND ? fmaxf(lo, 1.f) : copysignf(lo, x[k]);
+    a[k + 1] = SECOND ? fmaxf(hi, 1.f) : copysignf(hi, x[k + 1]);
+    const F2 a2 = pack2(a[k], a[k + 1]), z2 = add2(a2, up);
+    unpack2(z2, z[k], z[k + 1]);
+    unpack2(fma2(add2(z2, down), minus, a2), f[k], f[k + 1]);
+  }
+  return max_abs8(f) > (SECOND ? FAR_R : FAR_M);
+}
+
+template <bool STOCH>
+__device__ __forceinline__ void encode8_m_fast(const float (&m)[8], float inv, const uint32_t (&h)[4], uint32_t (&w)[2]) {
+  float a[8], z[8];
+  if (round8<false, STOCH>(m, inv, h, a, z)) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (fabsf(a[k] - (z[k] - ROUND_MAGIC)) > FAR_M) {
+        const uint32_t hk = (h[k >> 1] >> (16 * (k & 1))) & 0xFFFFu;
+        const float u = STOCH ? unit16(((hk >> 8) | (hk << 8)) & 0xFFFFu) : 0.5f;
+        z[k] = copysignf(fminf(real_code(fabsf(m[k]), inv, u), 127.f), m[k]) + ROUND_MAGIC;
+      }
+  }
+  w[0] = pack_low_bytes(z, 0);
+  w[1] = pack_low_bytes(z, 4);
+}
+
+template <bool STOCH>
+__device__ __forceinline__ void encode8_r_fast(const float (&v)[8], float inv, const uint32_t (&h)[4], uint32_t (&w)[2]) {
+  float r[8], a[8], z[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) r[k] = sqrt_fast(v[k]);
+  if (round8<true, STOCH>(r, inv, h, a, z)) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (fabsf(a[k] - (z[k] - (ROUND_MAGIC - 1.f))) > FAR_R) {
+        const float u = STOCH ? unit16((h[k >> 1] >> (16 * (k & 1))) & 0xFFFFu) : 0.5f;
+        z[k] = fminf(fmaxf(real_code(__fsqrt_rn(v[k]), inv, u), 1.f), 256.f) + (ROUND_MAGIC - 1.f);
+      }
+  }
+  w[0] = pack_low_bytes(z, 0);
+  w[1] = pack_low_bytes(z, 4);
+}
+
+// The moments that 8 codes stand for (decode_m, decode_r on all of them).
+__device__ __forceinline__ void decode8_m(const uint32_t (&w)[2], float s, float (&m)[8]) {
+  const uint32_t q[2] = {w[0] ^ 0x80808080u, w[1] ^ 0x80808080u};
+  const F2 bias = both(-8388736.f), s2 = both(s);      // 2^23 + 128
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) {
+    float lo, hi;
+    unpack2(add2(pack2(magic_byte(q[k >> 2], k & 3), magic_byte(q[k >> 2], (k & 3) + 1)), bias), lo, hi);
+    unpack2(mul2(pack2(__fmul_rn(lo, fabsf(lo)), __fmul_rn(hi, fabsf(hi))), s2), m[k], m[k + 1]);
+  }
+}
+
+__device__ __forceinline__ void decode8_v(const uint32_t (&w)[2], float s, float (&v)[8]) {
+  const F2 bias = both(-8388607.f), s2 = both(s);      // the code + 1
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) {
+    const F2 c = add2(pack2(magic_byte(w[k >> 2], k & 3), magic_byte(w[k >> 2], (k & 3) + 1)), bias);
+    const F2 r = mul2(mul2(c, c), s2);
+    unpack2(mul2(r, r), v[k], v[k + 1]);
+  }
+}
+
+// Blocks that the fast path takes: its flushes of subnormals then change no
+// code (an element whose v is subnormal lies below 2^-36 of the block's
+// largest, code 0 on either path).
+constexpr float FAST_V_MIN = 8.0779356694631609e-28f;   // 2^-90
+__device__ __forceinline__ bool fast_block(uint32_t mbits, uint32_t vbits) {
+  return mbits >= __float_as_uint(Q_TINY) && mbits < 0x7F800000u && vbits >= __float_as_uint(FAST_V_MIN) &&
+         vbits < 0x7F800000u;
+}
+
+// New moments, each operation rounded once.  A packed mul whose result goes
+// into a packed add is contracted to an fma whatever their rounding modifiers,
+// and so is an fma with a literal -0.  With a -0 that only the launch knows
+// the products stay products: adding it changes none.
+__device__ __forceinline__ void adam_moments8(float (&m)[8], float (&v)[8], const float (&g)[8], float scale,
+                                              const AdamPlanScalars& s) {
+  const F2 f = both(scale), b1 = both(s.beta1), o1 = both(s.one_beta1), b2 = both(s.beta2), o2 = both(s.one_beta2),
+           z = both(s.minus_zero);
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) {
+    const F2 g2 = mul2(pack2(g[k], g[k + 1]), f);
+    unpack2(add2(fma2(pack2(m[k], m[k + 1]), b1, z), fma2(g2, o1, z)), m[k], m[k + 1]);
+    unpack2(add2(fma2(pack2(v[k], v[k + 1]), b2, z), fma2(mul2(g2, g2), o2, z)), v[k], v[k + 1]);
+  }
+}
+
+// p <- p decay - step_size m / (sqrt(v) inv_bc2 + eps).  FAST: approximate
+// root and reciprocal (2^-22 of the update).
+template <bool FAST>
+__device__ __forceinline__ void adam_param8(float (&p)[8], const float (&m)[8], const float (&v)[8], float decay,
+                                            float step_size, float inv_bc2, float eps) {
+  const F2 d2 = both(decay), s2 = both(-step_size), c2 = both(inv_bc2), e2 = both(eps);
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) {
+    float lo, hi;
+    const F2 r = FAST ? pack2(sqrt_fast(v[k]), sqrt_fast(v[k + 1])) : pack2(__fsqrt_rn(v[k]), __fsqrt_rn(v[k + 1]));
+    unpack2(fma2(r, c2, e2), lo, hi);
+    const F2 q = FAST ? mul2(pack2(m[k], m[k + 1]), pack2(rcp_fast(lo), rcp_fast(hi))) : pack2(m[k] / lo, m[k + 1] / hi);
+    unpack2(fma2(pack2(p[k], p[k + 1]), d2, mul2(q, s2)), p[k], p[k + 1]);
+  }
 }
 
 // ---------------------------------------------------------------------------
 // AdamW
 // ---------------------------------------------------------------------------
 template <bool S8, bool PBF16, bool GBF16, bool STOCH>
-__global__ void __launch_bounds__(ST_THREADS)
+__global__ void __launch_bounds__(ST_THREADS, 4)
     adamw_plan_kernel(const AdamChunk* __restrict__ chunks, const __grid_constant__ GradPtrs grads,
                       const __grid_constant__ AdamPlanScalars sc, const int* flags) {
   // The table was complete before the first launch: it is read ahead of the
@@ -264,6 +470,8 @@ __global__ void __launch_bounds__(ST_THREADS)
     step_size = dyn[0]; inv_bc2 = dyn[1]; decay = dyn[2];
     step = dyn_step;
   }
+  // the fast path flushes a root below 2^-63 to zero: eps has to cover it
+  const bool eps_covers = sc.eps >= 2e-12f * inv_bc2;
   const uint32_t key = STOCH ? mix32(mix32(sc.seed_key + step) + ch.id) : 0u;
   const bool vec = aligned(ch.param, 16) && aligned(grad, 16) && aligned(ch.copy, 16) &&
                    aligned(ch.m, S8 ? 8 : 16) && aligned(ch.v, S8 ? 8 : 16);
@@ -273,8 +481,7 @@ __global__ void __launch_bounds__(ST_THREADS)
     const int e = b * Q_BLOCK + lane * 8;
     const int n = min(8, count - e);
     const bool full = vec && n == 8;
-    float g[8], p[8], m[8], v[8], r[8];
-    float ms = 0.f, vs = 0.f;
+    float g[8], p[8], m[8], v[8];
     char* pp = static_cast<char*>(ch.param) + int64_t(e) * (PBF16 ? 2 : 4);
     if (full) {
       load8_vec<GBF16>(grad + int64_t(e) * (GBF16 ? 2 : 4), g);
@@ -287,64 +494,76 @@ __global__ void __launch_bounds__(ST_THREADS)
       uint32_t mw[2], vw[2];
       load8_codes(static_cast<char*>(ch.m) + e, full, n, mw);
       load8_codes(static_cast<char*>(ch.v) + e, full, n, vw);
-      ms = ch.m_scale[b];
-      vs = ch.v_scale[b];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        m[k] = decode_m((mw[k >> 2] >> (8 * (k & 3))) & 0xFFu, ms);
-        const float r0 = decode_r((vw[k >> 2] >> (8 * (k & 3))) & 0xFFu, vs);
-        v[k] = __fmul_rn(r0, r0);
-      }
+      decode8_m(mw, ch.m_scale[b], m);
+      decode8_v(vw, ch.v_scale[b], v);
+    } else if (full) {
+      load8_vec<0>(static_cast<float*>(ch.m) + e, m);
+      load8_vec<0>(static_cast<float*>(ch.v) + e, v);
     } else {
-      if (full) {
-        load8_vec<0>(static_cast<float*>(ch.m) + e, m);
-        load8_vec<0>(static_cast<float*>(ch.v) + e, v);
-      } else {
-        load8_some<0>(static_cast<float*>(ch.m) + e, n, m);
-        load8_some<0>(static_cast<float*>(ch.v) + e, n, v);
-      }
+      load8_some<0>(static_cast<float*>(ch.m) + e, n, m);
+      load8_some<0>(static_cast<float*>(ch.v) + e, n, v);
     }
-    uint32_t mbits = 0, rbits = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      adam_moments(m[k], v[k], __fmul_rn(g[k], scale), sc);
-      r[k] = __fsqrt_rn(v[k]);
-      const float denom = fmaf(r[k], inv_bc2, sc.eps);
-      p[k] = fmaf(p[k], decay, -step_size * (m[k] / denom));
-      if (S8 && k < n) {
-        mbits = max(mbits, __float_as_uint(m[k]) & 0x7FFFFFFFu);
-        rbits = max(rbits, __float_as_uint(r[k]) & 0x7FFFFFFFu);
-      }
-    }
-    uint32_t h[4], hp[4];
+    adam_moments8(m, v, g, scale, sc);
+    if (eps_covers) adam_param8<true>(p, m, v, decay, step_size, inv_bc2, sc.eps);
+    else adam_param8<false>(p, m, v, decay, step_size, inv_bc2, sc.eps);
+    uint32_t h[4] = {};
     if (STOCH) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        h[k] = pair_bits(static_cast<uint64_t>(ch.base + e) / 2 + k, key);
-        hp[k] = PBF16 ? mix32(h[k] ^ 0x5BD1E995u) : 0u;
+      for (int k = 0; k < 4; ++k) h[k] = pair_bits(static_cast<uint64_t>(ch.base + e) / 2 + k, key);
+    }
+    if (n > 0) {
+      uint32_t w[4];
+      if (PBF16 && STOCH) {
+        const bool odd = !(max_abs8(p) < INFINITY);     // a carry would turn a NaN's bits into a number
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t hp = mix32(h[k] ^ 0x5BD1E995u);
+          if (odd)
+            w[k] = uint32_t(bf16_stochastic(p[2 * k], hp & 0xFFFFu)) | uint32_t(bf16_stochastic(p[2 * k + 1], hp >> 16)) << 16;
+          else
+            w[k] = __byte_perm(__float_as_uint(p[2 * k]) + (hp & 0xFFFFu), __float_as_uint(p[2 * k + 1]) + (hp >> 16), 0x7632);
+        }
+        store8_u16(pp, w, full, n);
+      } else if (PBF16 || ch.copy != nullptr) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = pack_bf16x2(p[2 * k], p[2 * k + 1]);
+        store8_u16(PBF16 ? static_cast<void*>(pp) : static_cast<void*>(ch.copy + e), w, full, n);
       }
+      if (!PBF16) store8_f32(reinterpret_cast<float*>(pp), p, full, n);
     }
     if (S8) {
-      mbits = __reduce_max_sync(0xffffffffu, mbits);
-      rbits = __reduce_max_sync(0xffffffffu, rbits);
+      // past the end m is 0 (no code, no gradient), but a code 0 of v is not
+      if (n < 8) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k >= n) v[k] = 0.f;
+      }
+      const uint32_t mbits = __reduce_max_sync(0xffffffffu, __float_as_uint(max_abs8(m)));
+      const uint32_t vbits = __reduce_max_sync(0xffffffffu, __float_as_uint(max_abs8(v)));
       float minv, rinv;
       const float mscale = block_scale(mbits, 1.f / 16129.f, minv);
-      const float rscale = block_scale(rbits, 1.f / 65536.f, rinv);
+      // roots keep order, so the largest root is the root of the largest
+      const float rscale = block_scale(__float_as_uint(__fsqrt_rn(__uint_as_float(vbits))), 1.f / 65536.f, rinv);
       if (lane == 0) {
         ch.m_scale[b] = mscale;
         ch.v_scale[b] = rscale;
       }
       uint32_t mw[2] = {0, 0}, vw[2] = {0, 0};
+      if (fast_block(mbits, vbits)) {
+        encode8_m_fast<STOCH>(m, minv, h, mw);
+        encode8_r_fast<STOCH>(v, rinv, h, vw);
+      } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        float um = 0.5f, uv = 0.5f;
-        if (STOCH) {
-          const uint32_t hk = (h[k >> 1] >> (16 * (k & 1))) & 0xFFFFu;
-          uv = unit16(hk);
-          um = unit16(((hk >> 8) | (hk << 8)) & 0xFFFFu);
+        for (int k = 0; k < 8; ++k) {
+          float um = 0.5f, uv = 0.5f;
+          if (STOCH) {
+            const uint32_t hk = (h[k >> 1] >> (16 * (k & 1))) & 0xFFFFu;
+            uv = unit16(hk);
+            um = unit16(((hk >> 8) | (hk << 8)) & 0xFFFFu);
+          }
+          mw[k >> 2] |= encode_m(m[k], minv, um) << (8 * (k & 3));
+          vw[k >> 2] |= encode_r(__fsqrt_rn(v[k]), rinv, uv) << (8 * (k & 3));
         }
-        mw[k >> 2] |= encode_m(m[k], minv, um) << (8 * (k & 3));
-        vw[k >> 2] |= encode_r(r[k], rinv, uv) << (8 * (k & 3));
       }
       if (n > 0) {
         store8_codes(static_cast<char*>(ch.m) + e, mw, full, n);
@@ -353,25 +572,6 @@ __global__ void __launch_bounds__(ST_THREADS)
     } else if (n > 0) {
       store8_f32(static_cast<float*>(ch.m) + e, m, full, n);
       store8_f32(static_cast<float*>(ch.v) + e, v, full, n);
-    }
-    if (n > 0) {
-      if (PBF16) {
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          w[k] = STOCH ? uint32_t(bf16_stochastic(p[2 * k], hp[k] & 0xFFFFu)) |
-                             uint32_t(bf16_stochastic(p[2 * k + 1], hp[k] >> 16)) << 16
-                       : pack_bf16x2(p[2 * k], p[2 * k + 1]);
-        store8_u16(pp, w, full, n);
-      } else {
-        store8_f32(reinterpret_cast<float*>(pp), p, full, n);
-        if (ch.copy != nullptr) {
-          uint32_t w[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = pack_bf16x2(p[2 * k], p[2 * k + 1]);
-          store8_u16(ch.copy + e, w, full, n);
-        }
-      }
     }
   }
 }

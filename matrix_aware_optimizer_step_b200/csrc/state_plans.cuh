@@ -309,6 +309,7 @@ muon_status muon_adamw_plan_step(muon_plan* plan, const muon_adamw_plan_hparams*
   sc.lr_ptr = lr_ptr;
   sc.grad_scale = grad_scale;
   sc.seed_key = mix32(seed);
+  sc.minus_zero = -0.f;
   GradPtrs g;
   ProfScope ps(ctx, MUON_K_ADAMW, st);
   for (const PlanBucket& b : plan->buckets) {
