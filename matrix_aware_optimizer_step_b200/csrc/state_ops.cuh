@@ -43,7 +43,12 @@ namespace muon {
 
 constexpr int ST_THREADS = 256;
 constexpr int Q_BLOCK = 256;            // elements that share a scale: one warp, 8 per lane
-constexpr int ST_CHUNK = 2048;          // elements of one thread block: a block of 256 for each warp
+constexpr int ST_WARPS = ST_THREADS / 32;
+constexpr int ADAM8_CTAS = 4;             // resident thread blocks per SM
+constexpr int ADAM8_SMEM = 55 * 1024;     // of shared memory each
+constexpr int STATE8_BLOCKS = 4;          // per warp
+constexpr int NORM_CHUNK = 8192;
+constexpr int NORM_CTAS = 8;              // resident thread blocks per SM
 constexpr int MAX_SLOTS = 480;          // tensors of one launch: their gradient pointers are a kernel
                                         // parameter (3840 B), so rebinding gradients touches no
                                         // device memory that a launch in flight could be reading
@@ -53,31 +58,36 @@ struct GradPtrs {
   const void* p[MAX_SLOTS];
 };
 
-// ST_CHUNK elements of one tensor.  Pointers are those of the chunk's first
-// element, so a block starts after one 64-byte load.
+// The work of one thread block: consecutive blocks of 256 elements of one
+// tensor, the same number for each of its warps.  Pointers are those of the
+// first element, so a thread block starts after one load; the hardware hands
+// them out in order, so the GPU works on neighbouring addresses at any time
+// and an SM that gets less bandwidth gets less work.  (Persistent warps over
+// a static split were measured too: a pure stream lost 6 to 12 % to the
+// slowest SMs.)
 struct alignas(16) AdamChunk {
-  void* param;
-  void* m;                 // float or int8_t
-  void* v;                 // float or uint8_t
-  float* m_scale;          // 8-bit: one per 256 elements
+  char* param;
+  char* m;                 // float or int8_t
+  char* v;                 // float or uint8_t
+  float* m_scale;          // 8-bit: one per block
   float* v_scale;
   __nv_bfloat16* copy;     // nullptr: none
   int64_t base;            // first element's index in its tensor
   uint32_t id;             // the tensor's place in the plan's list
   uint16_t slot;           // its gradient in the launch's GradPtrs
-  uint16_t count;          // elements, 1 .. ST_CHUNK
+  uint16_t count;          // elements
 };
 static_assert(sizeof(AdamChunk) == 64, "one chunk is two 32-byte sectors");
 
 struct AdamPlanScalars {
-  float beta1, one_beta1, beta2, one_beta2;   // 1 - beta formed in 64 bits
+  float2 beta1, one_beta1, beta2, one_beta2;  // each twice, for packed operations; 1 - beta formed in 64 bits
+  float2 eps2, minus_zero;                    // -0: adam_moments8
   float eps, decay, step_size, inv_bc2;       // 1 - lr wd, lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
   double ln_beta1, ln_beta2, lr, wd;          // for a step count or rate that lives on the device
   const int64_t* step_ptr;
   const float* lr_ptr;
   const float* grad_scale;
   uint32_t seed_key, step;                    // mixed seed, low bits of the step
-  float minus_zero;                           // -0 (adam_moments8)
 };
 
 // 32-bit mixer: xor-shifts and odd multiplications, each a bijection.
@@ -87,11 +97,6 @@ __device__ __host__ __forceinline__ uint32_t mix32(uint32_t x) {
   x ^= x >> 15;
   x *= 0x846CA68Bu;
   return x ^ (x >> 16);
-}
-
-// 16 + 16 hashed bits for elements 2 q and 2 q + 1 of a tensor with key k.
-__device__ __forceinline__ uint32_t pair_bits(uint64_t q, uint32_t key) {
-  return mix32((static_cast<uint32_t>(q) ^ key) + static_cast<uint32_t>(q >> 32) * 0x9E3779B9u);
 }
 
 __device__ __forceinline__ float unit16(uint32_t h) {
@@ -107,70 +112,88 @@ __device__ __forceinline__ uint16_t bf16_stochastic(float x, uint32_t h16) {
 }
 
 // ---------------------------------------------------------------------------
-// 8 consecutive elements of a lane
+// a lane's 8 elements of a block: 4 l .. 4 l + 3 and 128 + 4 l .. 128 + 4 l + 3
 // ---------------------------------------------------------------------------
-template <int BF16>
-__device__ __forceinline__ void load8_vec(const void* p, float (&x)[8]) {
-  if (BF16) {
-    const uint4 w = *static_cast<const uint4*>(p);
-    float2 f;
-    f = unpack_bf16x2(w.x); x[0] = f.x; x[1] = f.y;
-    f = unpack_bf16x2(w.y); x[2] = f.x; x[3] = f.y;
-    f = unpack_bf16x2(w.z); x[4] = f.x; x[5] = f.y;
-    f = unpack_bf16x2(w.w); x[6] = f.x; x[7] = f.y;
+// Every vector access of a warp then covers consecutive bytes, whatever the
+// element's size.  `full`: the block is whole and the pointer aligned to 4
+// elements; else element by element, those below `count` (of the block).
+constexpr int HALF = Q_BLOCK / 2;
+
+__device__ __forceinline__ bool inside(int lane, int k, int count) {
+  return 4 * lane + (k & 3) + (k >> 2) * HALF < count;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void load8(const char* block, int lane, bool full, int count, float (&x)[8]) {
+  if (full) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (BF16) {
+        const uint2 w = *reinterpret_cast<const uint2*>(block + 8 * lane + j * 2 * HALF);
+        const float2 a = unpack_bf16x2(w.x), b = unpack_bf16x2(w.y);
+        x[4 * j] = a.x; x[4 * j + 1] = a.y; x[4 * j + 2] = b.x; x[4 * j + 3] = b.y;
+      } else {
+        const float4 a = *reinterpret_cast<const float4*>(block + 16 * lane + j * 4 * HALF);
+        x[4 * j] = a.x; x[4 * j + 1] = a.y; x[4 * j + 2] = a.z; x[4 * j + 3] = a.w;
+      }
+    }
   } else {
-    const float4 a = static_cast<const float4*>(p)[0], b = static_cast<const float4*>(p)[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int e = 4 * lane + (k & 3) + (k >> 2) * HALF;
+      x[k] = e >= count ? 0.f
+             : BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(block)[e])
+                    : reinterpret_cast<const float*>(block)[e];
+    }
   }
 }
 
-template <int BF16>
-__device__ __forceinline__ void load8_some(const void* p, int n, float (&x)[8]) {
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    x[k] = k >= n ? 0.f : BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[k]) : static_cast<const float*>(p)[k];
-}
-
-__device__ __forceinline__ void store8_f32(float* p, const float (&x)[8], bool vec, int n) {
-  if (vec) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void store8_f32(char* block, int lane, bool full, int count, const float (&x)[8]) {
+  if (full) {
+    *reinterpret_cast<float4*>(block + 16 * lane) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(block + 16 * lane + 4 * HALF) = make_float4(x[4], x[5], x[6], x[7]);
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (k < n) p[k] = x[k];
+      if (inside(lane, k, count)) reinterpret_cast<float*>(block)[4 * lane + (k & 3) + (k >> 2) * HALF] = x[k];
   }
 }
 
-__device__ __forceinline__ void store8_u16(void* p, const uint32_t (&w)[4], bool vec, int n) {
-  if (vec) {
-    *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+// w: pairs of bf16
+__device__ __forceinline__ void store8_u16(char* block, int lane, bool full, int count, const uint32_t (&w)[4]) {
+  if (full) {
+    *reinterpret_cast<uint2*>(block + 8 * lane) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(block + 8 * lane + 2 * HALF) = make_uint2(w[2], w[3]);
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (k < n) static_cast<uint16_t*>(p)[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+      if (inside(lane, k, count))
+        reinterpret_cast<uint16_t*>(block)[4 * lane + (k & 3) + (k >> 2) * HALF] =
+            static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
   }
 }
 
-__device__ __forceinline__ void load8_codes(const void* p, bool vec, int n, uint32_t (&w)[2]) {
-  if (vec) {
-    const uint2 q = *static_cast<const uint2*>(p);
-    w[0] = q.x; w[1] = q.y;
+__device__ __forceinline__ void load8_codes(const char* block, int lane, bool full, int count, uint32_t (&w)[2]) {
+  if (full) {
+    w[0] = *reinterpret_cast<const uint32_t*>(block + 4 * lane);
+    w[1] = *reinterpret_cast<const uint32_t*>(block + 4 * lane + HALF);
   } else {
     w[0] = w[1] = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (k < n) w[k >> 2] |= static_cast<uint32_t>(static_cast<const uint8_t*>(p)[k]) << (8 * (k & 3));
+      if (inside(lane, k, count))
+        w[k >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(block[4 * lane + (k & 3) + (k >> 2) * HALF])) << (8 * (k & 3));
   }
 }
 
-__device__ __forceinline__ void store8_codes(void* p, const uint32_t (&w)[2], bool vec, int n) {
-  if (vec) {
-    *static_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+__device__ __forceinline__ void store8_codes(char* block, int lane, bool full, int count, const uint32_t (&w)[2]) {
+  if (full) {
+    *reinterpret_cast<uint32_t*>(block + 4 * lane) = w[0];
+    *reinterpret_cast<uint32_t*>(block + 4 * lane + HALF) = w[1];
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (k < n) static_cast<uint8_t*>(p)[k] = static_cast<uint8_t>(w[k >> 2] >> (8 * (k & 3)));
+      if (inside(lane, k, count)) block[4 * lane + (k & 3) + (k >> 2) * HALF] = static_cast<char>(w[k >> 2] >> (8 * (k & 3)));
   }
 }
 
@@ -190,17 +213,14 @@ __device__ __forceinline__ float decode_r(uint32_t code, float s) {
 }
 
 // Scale of a block from its largest magnitude (as bits: NaN sorts above
-// infinity, so it is not lost in the maximum), and the scale's reciprocal, 0
-// for a block that keeps no codes.
-__device__ __forceinline__ float block_scale(uint32_t max_bits, float inv_levels2, float& inv) {
-  const float big = __uint_as_float(max_bits);
-  inv = 0.f;
-  if (max_bits >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
-  if (big < Q_TINY) return 0.f;
-  const float s = __fmul_rn(big, inv_levels2);
-  inv = __frcp_rn(s);
-  return s;
+// infinity, so it is not lost in the maximum).
+__device__ __forceinline__ float block_scale(uint32_t max_bits, float inv_levels2) {
+  const float s = __fmul_rn(__uint_as_float(max_bits), inv_levels2);
+  return max_bits >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : max_bits < __float_as_uint(Q_TINY) ? 0.f : s;
 }
+
+// 1 / s, 0 for a block that keeps no codes.
+__device__ __forceinline__ float scale_inverse(float s) { return s > 0.f ? __frcp_rn(s) : 0.f; }
 
 // floor(sqrt(x / s) + u)
 __device__ __forceinline__ float real_code(float x, float inv, float u) {
@@ -228,14 +248,16 @@ __device__ __forceinline__ uint32_t encode_r(float r, float inv, float u) {
 // (FAR_* below, both sides' errors added up), the code is formed again by the
 // definition.  A 16-bit u enters as h / 2^16 - 1/2, short of its 2^-17.
 //
-// Errors in y, in units of 2^-23 relative unless absolute:
-//   m: sqrt.approx 1, IEEE root 1/2; times 127: 2.3e-5.  y + u: 2^-17 on the
-//      definition's side, 2^-18 here, 2^-17 for the missing part of u: 1.9e-5.
-//   r: r itself 1 + 1/2, r * inv twice 1/2, halved by the root: 1.25; the root
-//      1 + 1/2; times 256: 8.4e-5.  y + u: 2^-17 + 2^-17 + 2^-17: 2.3e-5
-//      (2^-16 each above 256 only where min() decides).
-constexpr float FAR_M = 0.5f - 6.1e-5f;
-constexpr float FAR_R = 0.5f - 1.9e-4f;
+// Errors of y on both sides together, relative in units of 2^-23 (an IEEE
+// operation has 1/2, an approximate one 1), halved by the root where they
+// stand under it:
+//   m: 1 / s 1.5, times m 1 -> 1.25; the root 1.5; times 127: 4.2e-5.  y + u:
+//      2^-17 in the definition, 2^-18 twice here, 2^-17 for the missing part
+//      of u: 2.3e-5.
+//   r: r 1.5, 1 / s 1.5, the product 1 -> 2; the root 1.5; times 256: 1.07e-4.
+//      y + u: three times 2^-17 and 2^-18: 2.7e-5.
+constexpr float FAR_M = 0.5f - 6.8e-5f;
+constexpr float FAR_R = 0.5f - 1.4e-4f;
 constexpr float ROUND_MAGIC = 12582912.f;   // 1.5 * 2^23
 
 __device__ __forceinline__ float sqrt_fast(float x) {
@@ -273,6 +295,18 @@ __device__ __forceinline__ F2 pack2(float lo, float hi) {
 }
 __device__ __forceinline__ void unpack2(F2 a, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v)); }
 __device__ __forceinline__ F2 both(float x) { return pack2(x, x); }
+
+// Constants of packed operations, in constant memory: operands from there
+// take neither registers nor the two moves that build a pair of literals.
+enum PairConst { K_BIAS_M, K_BIAS_V, K_UP_M, K_DOWN_M, K_UP_R, K_DOWN_R, K_MINUS, K_UNIT, K_CENTRE, K_COUNT };
+__constant__ float2 kPairs[K_COUNT] = {
+    {-8388736.f, -8388736.f},                                  // - (2^23 + 128): a signed code
+    {-8388607.f, -8388607.f},                                  // - 2^23 + 1: an unsigned code + 1
+    {ROUND_MAGIC, ROUND_MAGIC}, {-ROUND_MAGIC, -ROUND_MAGIC},
+    {ROUND_MAGIC - 1.f, ROUND_MAGIC - 1.f}, {1.f - ROUND_MAGIC, 1.f - ROUND_MAGIC},
+    {-1.f, -1.f}, {1.f / 65536.f, 1.f / 65536.f}, {-128.5f, -128.5f}};
+__device__ __forceinline__ F2 pair(const float2& x) { return {*reinterpret_cast<const uint64_t*>(&x)}; }
+__device__ __forceinline__ F2 pair(PairConst k) { return {*reinterpret_cast<const uint64_t*>(&kPairs[k])}; }
 __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
   F2 r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
@@ -294,10 +328,10 @@ __device__ __forceinline__ float magic_byte(uint32_t w, int k) {
   return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7650 | k));
 }
 
-// h / 2^16 - 1/2 of the low (or high) half of w, its bytes swapped for `swap`
-__device__ __forceinline__ float half_unit(uint32_t w, int high, bool swap) {
-  const int b0 = 2 * high + (swap ? 1 : 0), b1 = 2 * high + (swap ? 0 : 1);
-  return fmaf(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7600 | (b1 << 4) | b0)), 1.f / 65536.f, -128.5f);
+// 2^23 + h of the low and the high half of w, their bytes swapped for `swap`
+__device__ __forceinline__ F2 magic_halves(uint32_t w, bool swap) {
+  return pack2(__uint_as_float(__byte_perm(w, 0x4B000000u, swap ? 0x7601 : 0x7610)),
+               __uint_as_float(__byte_perm(w, 0x4B000000u, swap ? 0x7623 : 0x7632)));
 }
 
 __device__ __forceinline__ uint32_t pack_low_bytes(const float (&z)[8], int at) {
@@ -311,8 +345,8 @@ __device__ __forceinline__ uint32_t pack_low_bytes(const float (&z)[8], int at) 
 // any lies within the limits of a boundary.
 template <bool SECOND, bool STOCH>
 __device__ __forceinline__ bool round8(const float (&x)[8], float inv, const uint32_t (&h)[4], float (&a)[8], float (&z)[8]) {
-  constexpr float MAGIC = SECOND ? ROUND_MAGIC - 1.f : ROUND_MAGIC;
-  const F2 i2 = both(inv), up = both(MAGIC), down = both(-MAGIC), minus = both(-1.f);
+  const F2 i2 = both(inv), up = pair(SECOND ? K_UP_R : K_UP_M), down = pair(SECOND ? K_DOWN_R : K_DOWN_M),
+           minus = pair(K_MINUS);
   float f[8];
 #pragma unroll
   for (int k = 0; k < 8; k += 2) {
@@ -320,10 +354,9 @@ __device__ __forceinline__ bool round8(const float (&x)[8], float inv, const uin
     unpack2(mul2(pack2(x[k], x[k + 1]), i2), lo, hi);
     lo = sqrt_fast(fabsf(lo));
     hi = sqrt_fast(fabsf(hi));
-    if (STOCH) {
-      lo += half_unit(h[k >> 1], 0, !SECOND);
-      hi += half_unit(h[k >> 1], 1, !SECOND);
-    }
+    // + h / 2^16 - 1/2; the magic 2^23 leaves 128 of it
+    if (STOCH)
+      unpack2(fma2(magic_halves(h[k >> 1], !SECOND), pair(K_UNIT), add2(pack2(lo, hi), pair(K_CENTRE))), lo, hi);
     a[k] = SECOND ? fmaxf(lo, 1.f) : copysignf(lo, x[k]);
     a[k + 1] = SECOND ? fmaxf(hi, 1.f) : copysignf(hi, x[k + 1]);
     const F2 a2 = pack2(a[k], a[k + 1]), z2 = add2(a2, up);
@@ -333,35 +366,43 @@ __device__ __forceinline__ bool round8(const float (&x)[8], float inv, const uin
   return max_abs8(f) > (SECOND ? FAR_R : FAR_M);
 }
 
-template <bool STOCH>
-__device__ __forceinline__ void encode8_m_fast(const float (&m)[8], float inv, const uint32_t (&h)[4], uint32_t (&w)[2]) {
-  float a[8], z[8];
-  if (round8<false, STOCH>(m, inv, h, a, z)) {
+// Forms the codes that round8 could not be sure of by their definition, one a
+// pass: almost always a single one of a warp's 256.
+template <bool SECOND, bool STOCH>
+__device__ __forceinline__ void redo8(const float (&x)[8], float s, const uint32_t (&h)[4], const float (&a)[8], float (&z)[8]) {
+  constexpr float MAGIC = SECOND ? ROUND_MAGIC - 1.f : ROUND_MAGIC, FAR = SECOND ? FAR_R : FAR_M;
+  const float inv = __frcp_rn(s);
+  uint32_t todo = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) todo |= (fabsf(a[k] - (z[k] - MAGIC)) > FAR ? 1u : 0u) << k;
+  while (todo != 0) {
+    const int at = __ffs(todo) - 1;
+    todo &= todo - 1;
+    float v = 0.f;
+    uint32_t word = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (fabsf(a[k] - (z[k] - ROUND_MAGIC)) > FAR_M) {
-        const uint32_t hk = (h[k >> 1] >> (16 * (k & 1))) & 0xFFFFu;
-        const float u = STOCH ? unit16(((hk >> 8) | (hk << 8)) & 0xFFFFu) : 0.5f;
-        z[k] = copysignf(fminf(real_code(fabsf(m[k]), inv, u), 127.f), m[k]) + ROUND_MAGIC;
+      if (k == at) {
+        v = x[k];
+        word = h[k >> 1] >> (16 * (k & 1));
       }
+    word &= 0xFFFFu;
+    const float u = STOCH ? unit16(SECOND ? word : ((word >> 8) | (word << 8)) & 0xFFFFu) : 0.5f;
+    const float c = SECOND ? fminf(fmaxf(real_code(__fsqrt_rn(v), inv, u), 1.f), 256.f)
+                           : copysignf(fminf(real_code(fabsf(v), inv, u), 127.f), v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k == at) z[k] = c + MAGIC;
   }
-  w[0] = pack_low_bytes(z, 0);
-  w[1] = pack_low_bytes(z, 4);
 }
 
-template <bool STOCH>
-__device__ __forceinline__ void encode8_r_fast(const float (&v)[8], float inv, const uint32_t (&h)[4], uint32_t (&w)[2]) {
-  float r[8], a[8], z[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) r[k] = sqrt_fast(v[k]);
-  if (round8<true, STOCH>(r, inv, h, a, z)) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (fabsf(a[k] - (z[k] - (ROUND_MAGIC - 1.f))) > FAR_R) {
-        const float u = STOCH ? unit16((h[k >> 1] >> (16 * (k & 1))) & 0xFFFFu) : 0.5f;
-        z[k] = fminf(fmaxf(real_code(__fsqrt_rn(v[k]), inv, u), 1.f), 256.f) + (ROUND_MAGIC - 1.f);
-      }
-  }
+// Codes of 8 first moments (x = r = m) or second moments (x = v, r its fast
+// root) on the fast path.
+template <bool SECOND, bool STOCH>
+__device__ __forceinline__ void encode8_fast(const float (&x)[8], const float (&r)[8], float s, const uint32_t (&h)[4],
+                                             uint32_t (&w)[2]) {
+  float a[8], z[8];
+  if (round8<SECOND, STOCH>(r, rcp_fast(s), h, a, z)) redo8<SECOND, STOCH>(x, s, h, a, z);
   w[0] = pack_low_bytes(z, 0);
   w[1] = pack_low_bytes(z, 4);
 }
@@ -369,7 +410,7 @@ __device__ __forceinline__ void encode8_r_fast(const float (&v)[8], float inv, c
 // The moments that 8 codes stand for (decode_m, decode_r on all of them).
 __device__ __forceinline__ void decode8_m(const uint32_t (&w)[2], float s, float (&m)[8]) {
   const uint32_t q[2] = {w[0] ^ 0x80808080u, w[1] ^ 0x80808080u};
-  const F2 bias = both(-8388736.f), s2 = both(s);      // 2^23 + 128
+  const F2 bias = pair(K_BIAS_M), s2 = both(s);
 #pragma unroll
   for (int k = 0; k < 8; k += 2) {
     float lo, hi;
@@ -379,7 +420,7 @@ __device__ __forceinline__ void decode8_m(const uint32_t (&w)[2], float s, float
 }
 
 __device__ __forceinline__ void decode8_v(const uint32_t (&w)[2], float s, float (&v)[8]) {
-  const F2 bias = both(-8388607.f), s2 = both(s);      // the code + 1
+  const F2 bias = pair(K_BIAS_V), s2 = both(s);
 #pragma unroll
   for (int k = 0; k < 8; k += 2) {
     const F2 c = add2(pack2(magic_byte(w[k >> 2], k & 3), magic_byte(w[k >> 2], (k & 3) + 1)), bias);
@@ -403,8 +444,8 @@ __device__ __forceinline__ bool fast_block(uint32_t mbits, uint32_t vbits) {
 // the products stay products: adding it changes none.
 __device__ __forceinline__ void adam_moments8(float (&m)[8], float (&v)[8], const float (&g)[8], float scale,
                                               const AdamPlanScalars& s) {
-  const F2 f = both(scale), b1 = both(s.beta1), o1 = both(s.one_beta1), b2 = both(s.beta2), o2 = both(s.one_beta2),
-           z = both(s.minus_zero);
+  const F2 f = both(scale), b1 = pair(s.beta1), o1 = pair(s.one_beta1), b2 = pair(s.beta2), o2 = pair(s.one_beta2),
+           z = pair(s.minus_zero);
 #pragma unroll
   for (int k = 0; k < 8; k += 2) {
     const F2 g2 = mul2(pack2(g[k], g[k + 1]), f);
@@ -416,14 +457,15 @@ __device__ __forceinline__ void adam_moments8(float (&m)[8], float (&v)[8], cons
 // p <- p decay - step_size m / (sqrt(v) inv_bc2 + eps).  FAST: approximate
 // root and reciprocal (2^-22 of the update).
 template <bool FAST>
-__device__ __forceinline__ void adam_param8(float (&p)[8], const float (&m)[8], const float (&v)[8], float decay,
-                                            float step_size, float inv_bc2, float eps) {
-  const F2 d2 = both(decay), s2 = both(-step_size), c2 = both(inv_bc2), e2 = both(eps);
+__device__ __forceinline__ void adam_param8(float (&p)[8], const float (&m)[8], const float (&v)[8], float (&r)[8],
+                                            float decay, float step_size, float inv_bc2, const float2& eps) {
+  const F2 d2 = both(decay), s2 = both(-step_size), c2 = both(inv_bc2), e2 = pair(eps);
 #pragma unroll
   for (int k = 0; k < 8; k += 2) {
     float lo, hi;
-    const F2 r = FAST ? pack2(sqrt_fast(v[k]), sqrt_fast(v[k + 1])) : pack2(__fsqrt_rn(v[k]), __fsqrt_rn(v[k + 1]));
-    unpack2(fma2(r, c2, e2), lo, hi);
+    r[k] = FAST ? sqrt_fast(v[k]) : __fsqrt_rn(v[k]);
+    r[k + 1] = FAST ? sqrt_fast(v[k + 1]) : __fsqrt_rn(v[k + 1]);
+    unpack2(fma2(pack2(r[k], r[k + 1]), c2, e2), lo, hi);
     const F2 q = FAST ? mul2(pack2(m[k], m[k + 1]), pack2(rcp_fast(lo), rcp_fast(hi))) : pack2(m[k] / lo, m[k + 1] / hi);
     unpack2(fma2(pack2(p[k], p[k + 1]), d2, mul2(q, s2)), p[k], p[k + 1]);
   }
@@ -432,147 +474,260 @@ __device__ __forceinline__ void adam_param8(float (&p)[8], const float (&m)[8], 
 // ---------------------------------------------------------------------------
 // AdamW
 // ---------------------------------------------------------------------------
-template <bool S8, bool PBF16, bool GBF16, bool STOCH>
+// What a launch's scalars come to on the device.
+struct AdamNow {
+  float scale, step_size, inv_bc2, decay;
+  uint32_t step;
+  bool go;                 // false: nothing is written
+};
+
+// Every lane of a warp calls it.
+__device__ __forceinline__ AdamNow adam_now(const AdamPlanScalars& sc, const int* flags) {
+  AdamNow d{1.f, sc.step_size, sc.inv_bc2, sc.decay, sc.step, true};
+  const bool stop = halted(flags);
+  if (sc.grad_scale != nullptr) {
+    d.scale = *sc.grad_scale;
+    d.go = isfinite(d.scale);           // a gradient was not finite
+  }
+  if (sc.step_ptr != nullptr || sc.lr_ptr != nullptr) {
+    if ((threadIdx.x & 31) == 0) {
+      const double lr = sc.lr_ptr != nullptr ? static_cast<double>(*sc.lr_ptr) : sc.lr;
+      d.go = d.go && isfinite(lr);
+      d.decay = static_cast<float>(1.0 - lr * sc.wd);
+      if (sc.step_ptr != nullptr) {
+        const int64_t t = *sc.step_ptr;
+        d.go = d.go && t >= 1;
+        d.step = static_cast<uint32_t>(t);
+        d.step_size = static_cast<float>(lr / -expm1(static_cast<double>(t) * sc.ln_beta1));
+        d.inv_bc2 = static_cast<float>(1.0 / sqrt(-expm1(static_cast<double>(t) * sc.ln_beta2)));
+      } else {
+        d.step_size = static_cast<float>(lr * static_cast<double>(sc.step_size));   // 1 / (1 - beta1^t) there
+      }
+    }
+    d.go = __shfl_sync(0xffffffffu, d.go, 0);
+    d.decay = __shfl_sync(0xffffffffu, d.decay, 0);
+    d.step = __shfl_sync(0xffffffffu, d.step, 0);
+    d.step_size = __shfl_sync(0xffffffffu, d.step_size, 0);
+    d.inv_bc2 = __shfl_sync(0xffffffffu, d.inv_bc2, 0);
+  }
+  d.go = d.go && !stop;
+  return d;
+}
+
+// The hashed bits of a lane's four pairs of elements: 16 for either element of
+// pair q, mix32((low word of q ^ key) + high word of q * 0x9E3779B9).  e: the
+// block's first element in its tensor, a multiple of 256, so that a pair's
+// place in the block only sets zero bits of e / 2.
+__device__ __forceinline__ void block_bits(int64_t e, int lane, uint32_t key, uint32_t (&h)[4]) {
+  const uint64_t q = static_cast<uint64_t>(e) / 2;
+  const uint32_t low = static_cast<uint32_t>(q) ^ key ^ (2 * lane), high = static_cast<uint32_t>(q >> 32) * 0x9E3779B9u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) h[k] = mix32((low ^ ((k >> 1) * (HALF / 2) + (k & 1))) + high);
+}
+
+// New parameters to memory: bf16 (nearest or stochastic), or fp32 and its copy.
+template <bool PBF16, bool STOCH>
+__device__ __forceinline__ void store_param(char* param, __nv_bfloat16* copy, int lane, bool full, int count,
+                                            const float (&p)[8], const uint32_t (&h)[4]) {
+  uint32_t w[4];
+  if (PBF16 && STOCH) {
+    const bool odd = !(max_abs8(p) < INFINITY);     // a carry would turn a NaN's bits into a number
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t hp = mix32(h[k] ^ 0x5BD1E995u);
+      if (odd)
+        w[k] = uint32_t(bf16_stochastic(p[2 * k], hp & 0xFFFFu)) | uint32_t(bf16_stochastic(p[2 * k + 1], hp >> 16)) << 16;
+      else
+        w[k] = __byte_perm(__float_as_uint(p[2 * k]) + (hp & 0xFFFFu), __float_as_uint(p[2 * k + 1]) + (hp >> 16), 0x7632);
+    }
+    store8_u16(param, lane, full, count, w);
+  } else if (PBF16 || copy != nullptr) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = pack_bf16x2(p[2 * k], p[2 * k + 1]);
+    store8_u16(PBF16 ? param : reinterpret_cast<char*>(copy), lane, full, count, w);
+  }
+  if (!PBF16) store8_f32(param, lane, full, count, p);
+}
+
+// The approximate root flushes one below 2^-63 to zero: eps has to cover it.
+__device__ __forceinline__ bool eps_covers(float eps, float inv_bc2) { return eps >= 2e-12f * inv_bc2; }
+
+// r receives the roots of v.
+__device__ __forceinline__ void adam_param8(float (&p)[8], const float (&m)[8], const float (&v)[8], float (&r)[8],
+                                            const AdamNow& now, const AdamPlanScalars& sc) {
+  if (eps_covers(sc.eps, now.inv_bc2)) adam_param8<true>(p, m, v, r, now.decay, now.step_size, now.inv_bc2, sc.eps2);
+  else adam_param8<false>(p, m, v, r, now.decay, now.step_size, now.inv_bc2, sc.eps2);
+}
+
+// fp32 moments: a block of 256 per warp, loaded straight to registers.
+template <bool PBF16, bool GBF16, bool STOCH>
 __global__ void __launch_bounds__(ST_THREADS, 4)
-    adamw_plan_kernel(const AdamChunk* __restrict__ chunks, const __grid_constant__ GradPtrs grads,
-                      const __grid_constant__ AdamPlanScalars sc, const int* flags) {
+    adamw32_kernel(const AdamChunk* __restrict__ chunks, const __grid_constant__ GradPtrs grads,
+                   const __grid_constant__ AdamPlanScalars sc, const int* flags) {
+  constexpr int P = PBF16 ? 2 : 4, G = GBF16 ? 2 : 4;
   // The table was complete before the first launch: it is read ahead of the
   // wait for the previous kernel.
   const AdamChunk ch = chunks[blockIdx.x];
-  const char* grad = static_cast<const char*>(grads.p[ch.slot]) + ch.base * (GBF16 ? 2 : 4);
+  const int lane = threadIdx.x & 31, first = (threadIdx.x >> 5) * Q_BLOCK;
+  const int count = static_cast<int>(ch.count) - first;
+  if (count <= 0) return;
+  const char* grad = static_cast<const char*>(grads.p[ch.slot]) + (ch.base + first) * G;
+  char *const pp = ch.param + first * P, *const mp = ch.m + first * 4, *const vp = ch.v + first * 4;
+  const bool full = count >= Q_BLOCK && aligned(pp, 4 * P) && aligned(grad, 4 * G) && aligned(mp, 16) &&
+                    aligned(vp, 16) && aligned(ch.copy, 8);
+  float g[8], p[8], m[8], v[8], r[8];
   pdl_wait();
-  if (halted(flags)) return;
-  float scale = 1.f;
-  if (sc.grad_scale != nullptr) {
-    scale = *sc.grad_scale;
-    if (!isfinite(scale)) return;       // a gradient was not finite: nothing is written
+  load8<GBF16>(grad, lane, full, count, g);
+  load8<PBF16>(pp, lane, full, count, p);
+  load8<false>(mp, lane, full, count, m);
+  load8<false>(vp, lane, full, count, v);
+  const AdamNow now = adam_now(sc, flags);
+  if (!now.go) return;
+  adam_moments8(m, v, g, now.scale, sc);
+  adam_param8(p, m, v, r, now, sc);
+  store8_f32(mp, lane, full, count, m);
+  store8_f32(vp, lane, full, count, v);
+  uint32_t h[4] = {};
+  if (STOCH) block_bits(ch.base + first, lane, mix32(mix32(sc.seed_key + now.step) + ch.id), h);
+  store_param<PBF16, STOCH>(pp, ch.copy == nullptr ? nullptr : ch.copy + first, lane, full, count, p, h);
+}
+
+// 8-bit moments: up to Stage8::blocks blocks per warp, fetched whole into
+// shared memory by one bulk copy an array before the first is worked on.  One
+// block per warp left the start-up (about 210 instructions and two loads that
+// wait for one another) unpaid for: 134M elements, fp32 parameters, took 409
+// us with one block, 323 with two, 294 with three; as many as ADAM8_CTAS
+// resident thread blocks have shared memory for.
+template <bool PBF16, bool GBF16>
+struct Stage8 {
+  static constexpr int P = PBF16 ? 2 : 4, G = GBF16 ? 2 : 4;
+  static constexpr int blocks = ADAM8_SMEM / (ST_WARPS * Q_BLOCK * (P + G + 2));
+  static constexpr int off_g = P * Q_BLOCK * blocks, off_m = off_g + G * Q_BLOCK * blocks, off_v = off_m + Q_BLOCK * blocks,
+                       bytes = off_v + Q_BLOCK * blocks;
+  static constexpr int cta = ST_WARPS * bytes;
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar) : "memory");
+}
+
+// Waits for the warp's bulk copies.  After kWaitLimitNs it records that in the
+// context's flags, gives copies in flight as long again to land before the
+// shared memory is given back, and returns false.
+__device__ __forceinline__ bool bulk_wait(uint64_t* bar, int* flags) {
+  if (mbar_try_wait(bar, 0)) return true;
+  for (int turn = 0; turn < 2; ++turn) {
+    const uint64_t start = global_timer_ns();
+    while (global_timer_ns() - start <= kWaitLimitNs)
+      if (mbar_try_wait(bar, 0)) return turn == 0;
+    atomicOr(flags, kDevErrTimeout);
   }
-  float step_size = sc.step_size, inv_bc2 = sc.inv_bc2, decay = sc.decay;
-  uint32_t step = sc.step;
-  if (sc.step_ptr != nullptr || sc.lr_ptr != nullptr) {
-    __shared__ float dyn[3];
-    __shared__ uint32_t dyn_step;
-    __shared__ int dyn_ok;
-    if (threadIdx.x == 0) {
-      const int64_t t = sc.step_ptr != nullptr ? *sc.step_ptr : 0;
-      const double lr = sc.lr_ptr != nullptr ? static_cast<double>(*sc.lr_ptr) : sc.lr;
-      dyn_ok = (sc.step_ptr == nullptr || t >= 1) && isfinite(lr);
-      dyn_step = sc.step_ptr != nullptr ? static_cast<uint32_t>(t) : sc.step;
-      // host-side bias corrections stand in step_size / lr and inv_bc2
-      const double bc1 = sc.step_ptr != nullptr ? -expm1(static_cast<double>(t) * sc.ln_beta1) : 0.0;
-      const double bc2 = sc.step_ptr != nullptr ? -expm1(static_cast<double>(t) * sc.ln_beta2) : 0.0;
-      dyn[0] = static_cast<float>(sc.step_ptr != nullptr ? lr / bc1 : lr * static_cast<double>(sc.step_size));
-      dyn[1] = sc.step_ptr != nullptr ? static_cast<float>(1.0 / sqrt(bc2)) : sc.inv_bc2;
-      dyn[2] = static_cast<float>(1.0 - lr * sc.wd);
-    }
-    __syncthreads();
-    if (!dyn_ok) return;
-    step_size = dyn[0]; inv_bc2 = dyn[1]; decay = dyn[2];
-    step = dyn_step;
+  return false;
+}
+
+template <bool PBF16, bool GBF16, bool STOCH>
+__global__ void __launch_bounds__(ST_THREADS, ADAM8_CTAS)
+    adamw8_kernel(const AdamChunk* __restrict__ chunks, int blocks, const __grid_constant__ GradPtrs grads,
+                  const __grid_constant__ AdamPlanScalars sc, int* flags) {
+  using St = Stage8<PBF16, GBF16>;
+  extern __shared__ __align__(128) char smem[];
+  __shared__ __align__(8) uint64_t bars[ST_WARPS];
+  const AdamChunk ch = chunks[blockIdx.x];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = warp * blocks * Q_BLOCK;
+  int count = min(static_cast<int>(ch.count) - first, blocks * Q_BLOCK);
+  if (count <= 0) return;
+  const char* grad = static_cast<const char*>(grads.p[ch.slot]) + (ch.base + first) * St::G;
+  char *pp = ch.param + first * St::P, *mp = ch.m + first, *vp = ch.v + first;
+  float *ms = ch.m_scale + first / Q_BLOCK, *vs = ch.v_scale + first / Q_BLOCK;
+  __nv_bfloat16* cp = ch.copy == nullptr ? nullptr : ch.copy + first;
+  // bulk copies want 16-byte boundaries; whole blocks have them when their
+  // tensors do.  What is left (a tensor's last block, views at odd offsets) is
+  // loaded where it is used.
+  const bool vec = aligned(pp, 16) && aligned(grad, 16) && aligned(mp, 16) && aligned(vp, 16) && aligned(cp, 8);
+  const int whole = vec ? count / Q_BLOCK : 0;
+  const char* mine = smem + warp * St::bytes;
+  const uint32_t dst = smem_u32(mine), bar = smem_u32(&bars[warp]);
+  if (lane == 0) {
+    mbar_init(&bars[warp], 1);
+    fence_barrier_init();
   }
-  // the fast path flushes a root below 2^-63 to zero: eps has to cover it
-  const bool eps_covers = sc.eps >= 2e-12f * inv_bc2;
-  const uint32_t key = STOCH ? mix32(mix32(sc.seed_key + step) + ch.id) : 0u;
-  const bool vec = aligned(ch.param, 16) && aligned(grad, 16) && aligned(ch.copy, 16) &&
-                   aligned(ch.m, S8 ? 8 : 16) && aligned(ch.v, S8 ? 8 : 16);
-  const int lane = threadIdx.x & 31;
-  const int count = ch.count;
-  for (int b = threadIdx.x >> 5; b * Q_BLOCK < count; b += ST_THREADS / 32) {
-    const int e = b * Q_BLOCK + lane * 8;
-    const int n = min(8, count - e);
-    const bool full = vec && n == 8;
-    float g[8], p[8], m[8], v[8];
-    char* pp = static_cast<char*>(ch.param) + int64_t(e) * (PBF16 ? 2 : 4);
+  __syncwarp();
+  pdl_wait();
+  if (whole > 0 && lane == 0) {
+    const uint32_t n = whole * Q_BLOCK;
+    mbar_arrive_expect_tx(&bars[warp], n * (St::P + St::G + 2));
+    bulk_load(dst + St::off_g, grad, n * St::G, bar);
+    bulk_load(dst, pp, n * St::P, bar);
+    bulk_load(dst + St::off_m, mp, n, bar);
+    bulk_load(dst + St::off_v, vp, n, bar);
+  }
+  // the scales of all the warp's blocks, one per lane
+  float scales = 0.f;
+  if ((lane >> 1) * Q_BLOCK < count) scales = (lane & 1 ? vs : ms)[lane >> 1];
+  const AdamNow now = adam_now(sc, flags);
+  if (whole > 0 && !bulk_wait(&bars[warp], flags)) return;
+  if (!now.go) return;
+  const uint32_t key = STOCH ? mix32(mix32(sc.seed_key + now.step) + ch.id) : 0u;
+#pragma unroll 1
+  for (int b = 0; count > 0; ++b, count -= Q_BLOCK) {
+    const bool full = b < whole;
+    const int at = b * Q_BLOCK;
+    float g[8], p[8], m[8], v[8], r[8];
+    uint32_t mw[2], vw[2];
     if (full) {
-      load8_vec<GBF16>(grad + int64_t(e) * (GBF16 ? 2 : 4), g);
-      load8_vec<PBF16>(pp, p);
+      load8<GBF16>(mine + St::off_g + at * St::G, lane, true, Q_BLOCK, g);
+      load8<PBF16>(mine + at * St::P, lane, true, Q_BLOCK, p);
+      load8_codes(mine + St::off_m + at, lane, true, Q_BLOCK, mw);
+      load8_codes(mine + St::off_v + at, lane, true, Q_BLOCK, vw);
     } else {
-      load8_some<GBF16>(grad + int64_t(e) * (GBF16 ? 2 : 4), n, g);
-      load8_some<PBF16>(pp, n, p);
+      load8<GBF16>(grad + at * St::G, lane, false, count, g);
+      load8<PBF16>(pp + at * St::P, lane, false, count, p);
+      load8_codes(mp + at, lane, false, count, mw);
+      load8_codes(vp + at, lane, false, count, vw);
     }
-    if (S8) {
-      uint32_t mw[2], vw[2];
-      load8_codes(static_cast<char*>(ch.m) + e, full, n, mw);
-      load8_codes(static_cast<char*>(ch.v) + e, full, n, vw);
-      decode8_m(mw, ch.m_scale[b], m);
-      decode8_v(vw, ch.v_scale[b], v);
-    } else if (full) {
-      load8_vec<0>(static_cast<float*>(ch.m) + e, m);
-      load8_vec<0>(static_cast<float*>(ch.v) + e, v);
-    } else {
-      load8_some<0>(static_cast<float*>(ch.m) + e, n, m);
-      load8_some<0>(static_cast<float*>(ch.v) + e, n, v);
-    }
-    adam_moments8(m, v, g, scale, sc);
-    if (eps_covers) adam_param8<true>(p, m, v, decay, step_size, inv_bc2, sc.eps);
-    else adam_param8<false>(p, m, v, decay, step_size, inv_bc2, sc.eps);
+    decode8_m(mw, __shfl_sync(0xffffffffu, scales, 2 * b), m);
+    decode8_v(vw, __shfl_sync(0xffffffffu, scales, 2 * b + 1), v);
+    adam_moments8(m, v, g, now.scale, sc);
+    adam_param8(p, m, v, r, now, sc);
     uint32_t h[4] = {};
-    if (STOCH) {
+    if (STOCH) block_bits(ch.base + first + at, lane, key, h);
+    store_param<PBF16, STOCH>(pp + at * St::P, cp == nullptr ? nullptr : cp + at, lane, full, count, p, h);
+    // past the end m is 0 (no code, no gradient), but a code 0 of v is not
+    if (count < Q_BLOCK) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) h[k] = pair_bits(static_cast<uint64_t>(ch.base + e) / 2 + k, key);
+      for (int k = 0; k < 8; ++k)
+        if (!inside(lane, k, count)) v[k] = r[k] = 0.f;
     }
-    if (n > 0) {
-      uint32_t w[4];
-      if (PBF16 && STOCH) {
-        const bool odd = !(max_abs8(p) < INFINITY);     // a carry would turn a NaN's bits into a number
+    const uint32_t mbits = __reduce_max_sync(0xffffffffu, __float_as_uint(max_abs8(m)));
+    const uint32_t vbits = __reduce_max_sync(0xffffffffu, __float_as_uint(max_abs8(v)));
+    // even lanes form the scale of m, odd ones that of r.  (Roots keep order:
+    // the largest root is the root of the largest.)
+    const bool second = lane & 1;
+    const float mine_scale = block_scale(second ? __float_as_uint(__fsqrt_rn(__uint_as_float(vbits))) : mbits,
+                                         second ? 1.f / 65536.f : 1.f / 16129.f);
+    if (lane < 2) (second ? vs : ms)[b] = mine_scale;
+    const float mscale = __shfl_sync(0xffffffffu, mine_scale, 0), rscale = __shfl_sync(0xffffffffu, mine_scale, 1);
+    if (fast_block(mbits, vbits)) {
+      encode8_fast<false, STOCH>(m, m, mscale, h, mw);
+      encode8_fast<true, STOCH>(v, r, rscale, h, vw);
+    } else {
+      const float minv = scale_inverse(mscale), rinv = scale_inverse(rscale);
+      mw[0] = mw[1] = vw[0] = vw[1] = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t hp = mix32(h[k] ^ 0x5BD1E995u);
-          if (odd)
-            w[k] = uint32_t(bf16_stochastic(p[2 * k], hp & 0xFFFFu)) | uint32_t(bf16_stochastic(p[2 * k + 1], hp >> 16)) << 16;
-          else
-            w[k] = __byte_perm(__float_as_uint(p[2 * k]) + (hp & 0xFFFFu), __float_as_uint(p[2 * k + 1]) + (hp >> 16), 0x7632);
+      for (int k = 0; k < 8; ++k) {
+        float um = 0.5f, uv = 0.5f;
+        if (STOCH) {
+          const uint32_t hk = (h[k >> 1] >> (16 * (k & 1))) & 0xFFFFu;
+          uv = unit16(hk);
+          um = unit16(((hk >> 8) | (hk << 8)) & 0xFFFFu);
         }
-        store8_u16(pp, w, full, n);
-      } else if (PBF16 || ch.copy != nullptr) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = pack_bf16x2(p[2 * k], p[2 * k + 1]);
-        store8_u16(PBF16 ? static_cast<void*>(pp) : static_cast<void*>(ch.copy + e), w, full, n);
+        mw[k >> 2] |= encode_m(m[k], minv, um) << (8 * (k & 3));
+        vw[k >> 2] |= encode_r(__fsqrt_rn(v[k]), rinv, uv) << (8 * (k & 3));
       }
-      if (!PBF16) store8_f32(reinterpret_cast<float*>(pp), p, full, n);
     }
-    if (S8) {
-      // past the end m is 0 (no code, no gradient), but a code 0 of v is not
-      if (n < 8) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k >= n) v[k] = 0.f;
-      }
-      const uint32_t mbits = __reduce_max_sync(0xffffffffu, __float_as_uint(max_abs8(m)));
-      const uint32_t vbits = __reduce_max_sync(0xffffffffu, __float_as_uint(max_abs8(v)));
-      float minv, rinv;
-      const float mscale = block_scale(mbits, 1.f / 16129.f, minv);
-      // roots keep order, so the largest root is the root of the largest
-      const float rscale = block_scale(__float_as_uint(__fsqrt_rn(__uint_as_float(vbits))), 1.f / 65536.f, rinv);
-      if (lane == 0) {
-        ch.m_scale[b] = mscale;
-        ch.v_scale[b] = rscale;
-      }
-      uint32_t mw[2] = {0, 0}, vw[2] = {0, 0};
-      if (fast_block(mbits, vbits)) {
-        encode8_m_fast<STOCH>(m, minv, h, mw);
-        encode8_r_fast<STOCH>(v, rinv, h, vw);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float um = 0.5f, uv = 0.5f;
-          if (STOCH) {
-            const uint32_t hk = (h[k >> 1] >> (16 * (k & 1))) & 0xFFFFu;
-            uv = unit16(hk);
-            um = unit16(((hk >> 8) | (hk << 8)) & 0xFFFFu);
-          }
-          mw[k >> 2] |= encode_m(m[k], minv, um) << (8 * (k & 3));
-          vw[k >> 2] |= encode_r(__fsqrt_rn(v[k]), rinv, uv) << (8 * (k & 3));
-        }
-      }
-      if (n > 0) {
-        store8_codes(static_cast<char*>(ch.m) + e, mw, full, n);
-        store8_codes(static_cast<char*>(ch.v) + e, vw, full, n);
-      }
-    } else if (n > 0) {
-      store8_f32(static_cast<float*>(ch.m) + e, m, full, n);
-      store8_f32(static_cast<float*>(ch.v) + e, v, full, n);
-    }
+    store8_codes(mp + at, lane, full, count, mw);
+    store8_codes(vp + at, lane, full, count, vw);
   }
 }
 
@@ -580,93 +735,123 @@ __global__ void __launch_bounds__(ST_THREADS, 4)
 // conversion
 // ---------------------------------------------------------------------------
 struct alignas(16) Q8Chunk {
-  void* values;            // fp32 or bf16 moments
-  void* codes;             // int8 first moments or uint8 second moments
+  char* values;            // fp32 or bf16 moments
+  char* codes;             // int8 first moments or uint8 second moments
   float* scales;
-  uint16_t count;          // 1 .. ST_CHUNK
+  uint16_t count;          // elements
   uint8_t second;          // 1: second moments
   uint8_t bf16;            // values' type
   uint32_t pad;
 };
 static_assert(sizeof(Q8Chunk) == 32, "one chunk is one sector");
 
-// PACK: values -> codes and scales, rounded to nearest.  Else the values that
-// the codes stand for, rounded once to the values' type.
-template <bool PACK>
-__global__ void __launch_bounds__(ST_THREADS)
-    state8_kernel(const Q8Chunk* __restrict__ chunks, const int* flags) {
-  const Q8Chunk ch = chunks[blockIdx.x];
-  pdl_wait();
-  if (halted(flags)) return;
-  const int lane = threadIdx.x & 31;
-  const int count = ch.count;
-  const bool vec = aligned(ch.values, 16) && aligned(ch.codes, 8);
-  for (int b = threadIdx.x >> 5; b * Q_BLOCK < count; b += ST_THREADS / 32) {
-    const int e = b * Q_BLOCK + lane * 8;
-    const int n = min(8, count - e);
-    const bool full = vec && n == 8;
-    char* vp = static_cast<char*>(ch.values) + int64_t(e) * (ch.bf16 ? 2 : 4);
-    float x[8];
-    uint32_t w[2] = {0, 0};
-    if (PACK) {
-      if (ch.bf16) {
-        if (full) load8_vec<1>(vp, x); else load8_some<1>(vp, n, x);
+// One block.  PACK: values -> codes and scale, rounded to nearest.  Else the
+// values that the codes stand for, rounded once to the values' type.
+template <bool SECOND>
+__device__ __forceinline__ void pack8(float (&x)[8], float* scale, int lane, uint32_t (&w)[2]) {
+  const uint32_t xbits = __reduce_max_sync(0xffffffffu, __float_as_uint(max_abs8(x)));
+  bool plain = true;
+  if (SECOND) {
+    // a negative second moment has no root
+    float low = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) low = fminf(low, x[k]);
+    plain = __all_sync(0xffffffffu, low == 0.f);
+  }
+  const uint32_t bits = !plain ? 0x7FC00000u : SECOND ? __float_as_uint(__fsqrt_rn(__uint_as_float(xbits))) : xbits;
+  const float s = block_scale(bits, SECOND ? 1.f / 65536.f : 1.f / 16129.f);
+  if (lane == 0) *scale = s;
+  const uint32_t none[4] = {};
+  w[0] = w[1] = 0;
+  if (plain && fast_block(SECOND ? __float_as_uint(1.f) : xbits, SECOND ? xbits : __float_as_uint(1.f))) {
+    float r[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r[k] = SECOND ? sqrt_fast(x[k]) : x[k];
+    encode8_fast<SECOND, false>(x, r, s, none, w);
+  } else {
+    const float inv = scale_inverse(s);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      w[k >> 2] |= (SECOND ? encode_r(__fsqrt_rn(x[k]), inv, 0.5f) : encode_m(x[k], inv, 0.5f)) << (8 * (k & 3));
+  }
+}
+
+// A warp's blocks of a chunk, U at once: their loads first.
+template <bool PACK, bool SECOND, bool BF16, int U>
+__device__ __forceinline__ void convert_blocks(char* values, char* codes, float* scales, int lane, bool full, int count) {
+  constexpr int V = BF16 ? 2 : 4;
+  float x[U][8];
+  uint32_t w[U][2];
+  if (PACK) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) load8<BF16>(values + u * Q_BLOCK * V, lane, full, count, x[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      pack8<SECOND>(x[u], scales + u, lane, w[u]);
+      store8_codes(codes + u * Q_BLOCK, lane, full, count, w[u]);
+    }
+  } else {
+    float s[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      load8_codes(codes + u * Q_BLOCK, lane, full, count, w[u]);
+      s[u] = scales[u];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (SECOND) decode8_v(w[u], s[u], x[u]);
+      else decode8_m(w[u], s[u], x[u]);
+      if (BF16) {
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = pack_bf16x2(x[u][2 * k], x[u][2 * k + 1]);
+        store8_u16(values + u * Q_BLOCK * V, lane, full, count, o);
       } else {
-        if (full) load8_vec<0>(vp, x); else load8_some<0>(vp, n, x);
-      }
-      uint32_t bits = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (ch.second) x[k] = __fsqrt_rn(x[k]);
-        bits = max(bits, __float_as_uint(x[k]) & 0x7FFFFFFFu);   // 0 past the end
-      }
-      bits = __reduce_max_sync(0xffffffffu, bits);
-      float inv;
-      const float s = block_scale(bits, ch.second ? 1.f / 65536.f : 1.f / 16129.f, inv);
-      if (lane == 0) ch.scales[b] = s;
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        w[k >> 2] |= (ch.second ? encode_r(x[k], inv, 0.5f) : encode_m(x[k], inv, 0.5f)) << (8 * (k & 3));
-      if (n > 0) store8_codes(static_cast<char*>(ch.codes) + e, w, full, n);
-    } else {
-      load8_codes(static_cast<char*>(ch.codes) + e, full, n, w);
-      const float s = ch.scales[b];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t c = (w[k >> 2] >> (8 * (k & 3))) & 0xFFu;
-        if (ch.second) {
-          const float r = decode_r(c, s);
-          x[k] = __fmul_rn(r, r);
-        } else {
-          x[k] = decode_m(c, s);
-        }
-      }
-      if (n > 0) {
-        if (ch.bf16) {
-          uint32_t o[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) o[k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
-          store8_u16(vp, o, full, n);
-        } else {
-          store8_f32(reinterpret_cast<float*>(vp), x, full, n);
-        }
+        store8_f32(values + u * Q_BLOCK * V, lane, full, count, x[u]);
       }
     }
   }
 }
 
+template <bool PACK, bool SECOND, bool BF16>
+__device__ __forceinline__ void convert_run(const Q8Chunk& ch, int first, int lane) {
+  constexpr int V = BF16 ? 2 : 4, U = STATE8_BLOCKS;
+  char *values = ch.values + first * V, *codes = ch.codes + first;
+  float* scales = ch.scales + first / Q_BLOCK;
+  int count = min(static_cast<int>(ch.count) - first, U * Q_BLOCK);
+  const bool vec = aligned(values, 4 * V) && aligned(codes, 4);
+  if (vec && count == U * Q_BLOCK) {
+    convert_blocks<PACK, SECOND, BF16, U>(values, codes, scales, lane, true, Q_BLOCK);
+    return;
+  }
+  for (; count > 0; count -= Q_BLOCK) {
+    convert_blocks<PACK, SECOND, BF16, 1>(values, codes, scales, lane, vec && count >= Q_BLOCK, count);
+    values += Q_BLOCK * V;
+    codes += Q_BLOCK;
+    ++scales;
+  }
+}
+
+template <bool PACK>
+__global__ void __launch_bounds__(ST_THREADS) state8_kernel(const Q8Chunk* __restrict__ chunks, const int* flags) {
+  const Q8Chunk ch = chunks[blockIdx.x];
+  const int lane = threadIdx.x & 31, first = (threadIdx.x >> 5) * STATE8_BLOCKS * Q_BLOCK;
+  pdl_wait();
+  if (first >= ch.count || halted(flags)) return;
+  if (ch.second)
+    ch.bf16 ? convert_run<PACK, true, true>(ch, first, lane) : convert_run<PACK, true, false>(ch, first, lane);
+  else
+    ch.bf16 ? convert_run<PACK, false, true>(ch, first, lane) : convert_run<PACK, false, false>(ch, first, lane);
+}
+
 // ---------------------------------------------------------------------------
 // gradient norm
 // ---------------------------------------------------------------------------
-constexpr int NORM_CHUNK = 8192;
-constexpr int NORM_BLOCKS_PER_SM = 8;
-
-struct NormChunk {
-  int64_t base;
+struct alignas(16) NormChunk {
+  int64_t base;            // first element's index in its tensor
   uint16_t slot;
   uint16_t count;          // 1 .. NORM_CHUNK
-  uint8_t bf16;
-  uint8_t pad[3];
+  uint32_t bf16;
 };
 static_assert(sizeof(NormChunk) == 16, "");
 
@@ -696,7 +881,7 @@ __device__ __forceinline__ double block_sum_f64(double v, double* red) {
   __syncthreads();
   double s = 0.0;
   if (threadIdx.x < 32) {
-    s = threadIdx.x < ST_THREADS / 32 ? red[threadIdx.x] : 0.0;
+    s = threadIdx.x < ST_WARPS ? red[threadIdx.x] : 0.0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   }
@@ -715,35 +900,65 @@ struct NormOut {
   unsigned int total;      // blocks of all launches (0: nothing to sum)
 };
 
-__global__ void __launch_bounds__(ST_THREADS)
-    grad_norm_kernel(const NormChunk* __restrict__ chunks, unsigned int nchunks,
-                     const __grid_constant__ GradPtrs grads, const NormOut o) {
-  __shared__ double red[ST_THREADS / 32];
-  __shared__ bool last;
-  pdl_wait();
+// One chunk: a thread's vectors of 16 bytes are ST_THREADS vectors apart, U
+// loaded at once.
+template <bool BF16>
+__device__ __forceinline__ double square_chunk(const char* g, int count) {
+  constexpr int N = BF16 ? 8 : 4, U = 8, V = NORM_CHUNK / N / ST_THREADS;    // elements and vectors of a thread
   double acc = 0.0;
-  for (unsigned int c = blockIdx.x; c < nchunks; c += gridDim.x) {
-    const NormChunk ch = chunks[c];
-    const int size = ch.bf16 ? 2 : 4;
-    const char* g = static_cast<const char*>(grads.p[ch.slot]) + ch.base * size;
-    const bool vec = aligned(g, 16);
+  if (count == NORM_CHUNK && aligned(g, 16)) {
+    const uint4* p = reinterpret_cast<const uint4*>(g) + threadIdx.x;
 #pragma unroll
-    for (int it = 0; it < NORM_CHUNK / (8 * ST_THREADS); ++it) {
-      const int e = (it * ST_THREADS + threadIdx.x) * 8;
-      const int n = min(8, int(ch.count) - e);
-      float x[8];
-      if (n <= 0) continue;
-      if (ch.bf16) {
-        if (vec && n == 8) load8_vec<1>(g + int64_t(e) * 2, x); else load8_some<1>(g + int64_t(e) * 2, n, x);
-      } else {
-        if (vec && n == 8) load8_vec<0>(g + int64_t(e) * 4, x); else load8_some<0>(g + int64_t(e) * 4, n, x);
+    for (int i = 0; i < V; i += U) {
+      uint4 raw[U];
+#pragma unroll
+      for (int u = 0; u < U && i + u < V; ++u) raw[u] = p[(i + u) * ST_THREADS];
+#pragma unroll
+      for (int u = 0; u < U && i + u < V; u += BF16 ? 1 : 2) {
+        float x[8];
+        if (BF16) {
+          const float2 a = unpack_bf16x2(raw[u].x), b = unpack_bf16x2(raw[u].y), c = unpack_bf16x2(raw[u].z),
+                       d = unpack_bf16x2(raw[u].w);
+          x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y; x[4] = c.x; x[5] = c.y; x[6] = d.x; x[7] = d.y;
+        } else {
+          const uint4 w = raw[u], z = raw[u + 1 < U ? u + 1 : u];
+          x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y); x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
+          x[4] = __uint_as_float(z.x); x[5] = __uint_as_float(z.y); x[6] = __uint_as_float(z.z); x[7] = __uint_as_float(z.w);
+        }
+        acc += squares8(x);
       }
-      acc += squares8(x);
     }
+    return acc;
+  }
+  for (int b = (threadIdx.x >> 5) * Q_BLOCK; b < count; b += ST_THREADS * 8) {
+    float x[8];
+    const char* block = g + b * (BF16 ? 2 : 4);
+    load8<BF16>(block, threadIdx.x & 31, count - b >= Q_BLOCK && aligned(block, 16), count - b, x);
+    acc += squares8(x);
+  }
+  return acc;
+}
+
+// Thread block b takes chunks b, b + gridDim.x, ...
+__global__ void __launch_bounds__(ST_THREADS)
+    grad_norm_kernel(const NormChunk* __restrict__ chunks, unsigned nchunks, const __grid_constant__ GradPtrs grads,
+                     const NormOut o) {
+  __shared__ double red[ST_WARPS];
+  __shared__ bool last;
+  double acc = 0.0;
+  NormChunk ch{};
+  if (blockIdx.x < nchunks) ch = chunks[blockIdx.x];
+  pdl_wait();
+  for (unsigned c = blockIdx.x; c < nchunks;) {
+    const char* g = static_cast<const char*>(grads.p[ch.slot]) + ch.base * (ch.bf16 ? 2 : 4);
+    const NormChunk now = ch;
+    c += gridDim.x;
+    if (c < nchunks) ch = chunks[c];
+    acc += now.bf16 ? square_chunk<true>(g, now.count) : square_chunk<false>(g, now.count);
   }
   const double mine = block_sum_f64(acc, red);
   if (threadIdx.x == 0) {
-    if (nchunks > 0) o.partials[o.first + blockIdx.x] = mine;
+    if (o.total > 0) o.partials[o.first + blockIdx.x] = mine;
     __threadfence();
     // wraps to 0 when every block has come by
     last = o.total == 0 || atomicInc(o.counter, o.total - 1) == o.total - 1;

@@ -20,7 +20,8 @@ enum PlanKind { PLAN_ADAMW, PLAN_NORM, PLAN_STATE8 };
 struct PlanBucket {
   int pbf16 = 0, gbf16 = 0;
   std::vector<int> tensors;      // places in the plan's list; index = slot
-  int64_t first = 0, chunks = 0;
+  size_t first = 0, chunks = 0;  // in the plan's table
+  int blocks = 1;                // of 256 elements, per warp (AdamW)
 };
 
 struct muon_plan {
@@ -34,8 +35,8 @@ struct muon_plan {
   std::vector<int> grad_size;        // bytes of one element
   std::vector<std::pair<uintptr_t, uintptr_t>> written;   // sorted, disjoint
   std::vector<PlanBucket> buckets;
-  std::vector<unsigned> norm_grid;   // blocks per bucket
-  unsigned norm_blocks = 0;
+  std::vector<unsigned> norm_grid;
+  unsigned norm_ctas = 0;        // of all launches
 };
 
 namespace {
@@ -55,7 +56,6 @@ struct DeviceGuard {
 };
 
 constexpr int64_t kMaxNumel = int64_t(1) << 40;
-constexpr int64_t kMaxChunks = (int64_t(1) << 31) - 1;
 
 bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -83,9 +83,13 @@ void add_span(std::vector<Span>& v, const void* p, int64_t bytes, bool writes) {
 
 int dtype_size(int dt) { return dt == MUON_BF16 ? 2 : 4; }
 
-// Upload the chunk table and register the plan with its context.
+constexpr size_t kMaxChunks = (size_t(1) << 31) - 1;   // blocks of one launch
+
+// Upload the table and register the plan with its context.
 template <typename T>
 muon_status finish_plan(muon_ctx* ctx, muon_plan* plan, const std::vector<T>& table, muon_plan** out) {
+  for (const PlanBucket& b : plan->buckets)
+    if (b.chunks > kMaxChunks) return fail(ctx, MUON_ERR_UNSUPPORTED, "more elements than one launch covers");
   if (!table.empty()) {
     CUDA_TRY(ctx, cudaMalloc(&plan->table, table.size() * sizeof(T)));
     cudaError_t e = cudaMemcpyAsync(plan->table, table.data(), table.size() * sizeof(T), cudaMemcpyHostToDevice,
@@ -155,13 +159,27 @@ PlanBucket& bucket_for(muon_plan* plan, int pbf16, int gbf16) {
 }
 
 template <bool S8, bool P, bool G, bool ST>
-cudaError_t launch_adamw(const AdamChunk* t, int64_t n, const GradPtrs& g, const AdamPlanScalars& sc, const int* flags,
-                         cudaStream_t st) {
-  return launch_pdl(adamw_plan_kernel<S8, P, G, ST>, dim3(unsigned(n)), dim3(ST_THREADS), size_t(0), st, t, g, sc,
-                    flags);
+cudaError_t launch_adamw(const muon_plan* plan, const PlanBucket& b, const GradPtrs& g, const AdamPlanScalars& sc,
+                         int* flags, cudaStream_t st) {
+  const AdamChunk* t = static_cast<const AdamChunk*>(plan->table) + b.first;
+  const dim3 grid{unsigned(b.chunks)};
+  if constexpr (S8) {
+    constexpr int smem = Stage8<P, G>::cta;
+    static bool done[64] = {};
+    const int dev = plan->device & 63;
+    if (!done[dev]) {
+      const cudaError_t e = cudaFuncSetAttribute(adamw8_kernel<P, G, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+      done[dev] = true;
+    }
+    return launch_pdl(adamw8_kernel<P, G, ST>, grid, dim3(ST_THREADS), size_t(smem), st, t, b.blocks, g, sc, flags);
+  } else {
+    return launch_pdl(adamw32_kernel<P, G, ST>, grid, dim3(ST_THREADS), size_t(0), st, t, g, sc,
+                      static_cast<const int*>(flags));
+  }
 }
 
-using AdamLaunch = cudaError_t (*)(const AdamChunk*, int64_t, const GradPtrs&, const AdamPlanScalars&, const int*,
+using AdamLaunch = cudaError_t (*)(const muon_plan*, const PlanBucket&, const GradPtrs&, const AdamPlanScalars&, int*,
                                    cudaStream_t);
 
 // Stochastic rounding concerns codes and bf16 parameters: fp32 moments on fp32
@@ -237,13 +255,22 @@ muon_status muon_adamw_plan_create(muon_ctx* ctx, const muon_plan_tensor* tensor
       return fail(ctx, MUON_ERR_INVALID_ARG, "a tensor that the step writes overlaps another tensor of the plan");
     for (const Span& s : spans)
       if (s.writes) plan->written.push_back({s.lo, s.hi});
+    // 8-bit: as many blocks per warp as give the resident warps one turn, up
+    // to what their shared memory holds; few blocks are spread over more warps
+    int64_t total = 0;
+    for (int i = 0; i < n; ++i) total += cdiv(tensors[i].numel, int64_t(Q_BLOCK));
+    const int64_t turn = total / (int64_t(device_sms(ctx->device)) * ADAM8_CTAS * ST_WARPS);
     std::vector<AdamChunk> table;
     for (PlanBucket& b : plan->buckets) {
-      b.first = int64_t(table.size());
+      b.first = table.size();
+      const int most = b.pbf16 ? (b.gbf16 ? Stage8<true, true>::blocks : Stage8<true, false>::blocks)
+                               : (b.gbf16 ? Stage8<false, true>::blocks : Stage8<false, false>::blocks);
+      b.blocks = s8 ? int(std::min<int64_t>(std::max<int64_t>(turn, 1), most)) : 1;
+      const int64_t chunk = int64_t(b.blocks) * ST_WARPS * Q_BLOCK;
       for (size_t k = 0; k < b.tensors.size(); ++k) {
         const muon_plan_tensor& t = tensors[b.tensors[k]];
         const int64_t es = s8 ? 1 : 4;
-        for (int64_t at = 0; at < t.numel; at += ST_CHUNK) {
+        for (int64_t at = 0; at < t.numel; at += chunk) {
           AdamChunk c{};
           c.param = static_cast<char*>(t.param) + at * dtype_size(t.param_dtype);
           c.m = static_cast<char*>(t.exp_avg) + at * es;
@@ -254,12 +281,11 @@ muon_status muon_adamw_plan_create(muon_ctx* ctx, const muon_plan_tensor* tensor
           c.base = at;
           c.id = uint32_t(b.tensors[k]);
           c.slot = uint16_t(k);
-          c.count = uint16_t(std::min<int64_t>(ST_CHUNK, t.numel - at));
+          c.count = uint16_t(std::min<int64_t>(chunk, t.numel - at));
           table.push_back(c);
         }
       }
-      b.chunks = int64_t(table.size()) - b.first;
-      if (b.chunks > kMaxChunks) return fail(ctx, MUON_ERR_UNSUPPORTED, "more elements than one launch covers");
+      b.chunks = table.size() - b.first;
     }
     return finish_plan(ctx, plan, table, out);
   });
@@ -289,11 +315,14 @@ muon_status muon_adamw_plan_step(muon_plan* plan, const muon_adamw_plan_hparams*
   ctx->last_stream = st;
   CUDA_TRY(ctx, cudaGetLastError());
   AdamPlanScalars sc{};
-  sc.beta1 = float(hp->beta1);
-  sc.one_beta1 = float(1.0 - hp->beta1);
-  sc.beta2 = float(hp->beta2);
-  sc.one_beta2 = float(1.0 - hp->beta2);
+  auto twice = [](double x) { return make_float2(float(x), float(x)); };
+  sc.beta1 = twice(hp->beta1);
+  sc.one_beta1 = twice(1.0 - hp->beta1);
+  sc.beta2 = twice(hp->beta2);
+  sc.one_beta2 = twice(1.0 - hp->beta2);
   sc.eps = float(hp->eps);
+  sc.eps2 = twice(hp->eps);
+  sc.minus_zero = twice(-0.0);
   sc.decay = float(1.0 - hp->lr * hp->weight_decay);
   sc.lr = hp->lr;
   sc.wd = hp->weight_decay;
@@ -309,13 +338,12 @@ muon_status muon_adamw_plan_step(muon_plan* plan, const muon_adamw_plan_hparams*
   sc.lr_ptr = lr_ptr;
   sc.grad_scale = grad_scale;
   sc.seed_key = mix32(seed);
-  sc.minus_zero = -0.f;
   GradPtrs g;
   ProfScope ps(ctx, MUON_K_ADAMW, st);
   for (const PlanBucket& b : plan->buckets) {
     fill_grads(plan, b, g);
     const AdamLaunch f = adamw_launcher(plan->state_bits == 8, b.pbf16, b.gbf16, stochastic != 0);
-    CUDA_TRY(ctx, f(static_cast<const AdamChunk*>(plan->table) + b.first, b.chunks, g, sc, ctx->dflags, st));
+    CUDA_TRY(ctx, f(plan, b, g, sc, ctx->dflags, st));
     ctx->launches++;
   }
   return MUON_OK;
@@ -340,24 +368,18 @@ muon_status muon_grad_norm_plan_create(muon_ctx* ctx, const muon_grad_tensor* te
       bucket_for(plan, 0, 0).tensors.push_back(i);
     }
     std::vector<NormChunk> table;
-    const int64_t most = int64_t(device_sms(ctx->device)) * NORM_BLOCKS_PER_SM;
+    const size_t most = size_t(device_sms(ctx->device)) * NORM_CTAS;
     for (PlanBucket& b : plan->buckets) {
-      b.first = int64_t(table.size());
+      b.first = table.size();
       for (size_t k = 0; k < b.tensors.size(); ++k) {
         const muon_grad_tensor& t = tensors[b.tensors[k]];
-        for (int64_t at = 0; at < t.numel; at += NORM_CHUNK) {
-          NormChunk c{};
-          c.base = at;
-          c.slot = uint16_t(k);
-          c.count = uint16_t(std::min<int64_t>(NORM_CHUNK, t.numel - at));
-          c.bf16 = t.grad_dtype == MUON_BF16;
-          table.push_back(c);
-        }
+        for (int64_t at = 0; at < t.numel; at += NORM_CHUNK)
+          table.push_back({at, uint16_t(k), uint16_t(std::min<int64_t>(NORM_CHUNK, t.numel - at)),
+                           t.grad_dtype == MUON_BF16 ? 1u : 0u});
       }
-      b.chunks = int64_t(table.size()) - b.first;
-      if (b.chunks > kMaxChunks) return fail(ctx, MUON_ERR_UNSUPPORTED, "more elements than one launch covers");
+      b.chunks = table.size() - b.first;
       plan->norm_grid.push_back(unsigned(std::min(b.chunks, most)));
-      plan->norm_blocks += plan->norm_grid.back();
+      plan->norm_ctas += plan->norm_grid.back();
     }
     return finish_plan(ctx, plan, table, out);
   });
@@ -365,7 +387,7 @@ muon_status muon_grad_norm_plan_create(muon_ctx* ctx, const muon_grad_tensor* te
 
 muon_status muon_grad_norm_out_bytes(const muon_plan* plan, size_t* bytes) {
   if (!plan || !bytes || plan->kind != PLAN_NORM) return MUON_ERR_INVALID_ARG;
-  *bytes = 16 + size_t(plan->norm_blocks) * sizeof(double);
+  *bytes = 16 + size_t(plan->norm_ctas) * sizeof(double);
   return MUON_OK;
 }
 
@@ -388,18 +410,21 @@ muon_status muon_grad_norm_run(muon_plan* plan, double max_norm, float* out, voi
   o.counter = reinterpret_cast<unsigned int*>(out + 2);
   o.partials = reinterpret_cast<double*>(out + 4);
   o.max_norm = max_norm;
-  o.total = plan->norm_blocks;
+  o.total = plan->norm_ctas;
   GradPtrs g;
   ProfScope ps(ctx, MUON_K_OTHER, st);
-  for (size_t k = 0; k < std::max<size_t>(1, plan->buckets.size()); ++k) {
-    const bool any = !plan->buckets.empty();
-    if (any) fill_grads(plan, plan->buckets[k], g);
-    const unsigned grid = any ? plan->norm_grid[k] : 1u;
-    const NormChunk* t = any ? static_cast<const NormChunk*>(plan->table) + plan->buckets[k].first : nullptr;
-    CUDA_TRY(ctx, launch_pdl(grad_norm_kernel, dim3(grid), dim3(ST_THREADS), size_t(0), st, t,
-                             any ? unsigned(plan->buckets[k].chunks) : 0u, g, o));
+  for (size_t k = 0; k < plan->buckets.size(); ++k) {
+    const PlanBucket& b = plan->buckets[k];
+    fill_grads(plan, b, g);
+    CUDA_TRY(ctx, launch_pdl(grad_norm_kernel, dim3(plan->norm_grid[k]), dim3(ST_THREADS), size_t(0), st,
+                             static_cast<const NormChunk*>(plan->table) + b.first, unsigned(b.chunks), g, o));
     ctx->launches++;
-    o.first += grid;
+    o.first += plan->norm_grid[k];
+  }
+  if (plan->buckets.empty()) {     // nothing to sum: norm 0
+    CUDA_TRY(ctx, launch_pdl(grad_norm_kernel, dim3(1), dim3(ST_THREADS), size_t(0), st,
+                             static_cast<const NormChunk*>(nullptr), 0u, g, o));
+    ctx->launches++;
   }
   return MUON_OK;
 }
@@ -431,6 +456,7 @@ muon_status muon_state8_plan_create(muon_ctx* ctx, const muon_state8_tensor* ten
     if (n < 0 || (n > 0 && !tensors)) return fail(ctx, MUON_ERR_INVALID_ARG, "bad tensor list");
     std::vector<Span> spans;
     std::vector<Q8Chunk> table;
+    constexpr int64_t chunk = int64_t(STATE8_BLOCKS) * ST_WARPS * Q_BLOCK;
     for (int i = 0; i < n; ++i) {
       const muon_state8_tensor& t = tensors[i];
       if (t.numel < 0 || t.numel > kMaxNumel)
@@ -446,12 +472,12 @@ muon_status muon_state8_plan_create(muon_ctx* ctx, const muon_state8_tensor* ten
       add_span(spans, t.values, t.numel * dtype_size(t.value_dtype), true);
       add_span(spans, t.codes, t.numel, true);
       add_span(spans, t.scales, cdiv(t.numel, Q_BLOCK) * 4, true);
-      for (int64_t at = 0; at < t.numel; at += ST_CHUNK) {
+      for (int64_t at = 0; at < t.numel; at += chunk) {
         Q8Chunk c{};
         c.values = static_cast<char*>(t.values) + at * dtype_size(t.value_dtype);
         c.codes = static_cast<char*>(t.codes) + at;
         c.scales = t.scales + at / Q_BLOCK;
-        c.count = uint16_t(std::min<int64_t>(ST_CHUNK, t.numel - at));
+        c.count = uint16_t(std::min<int64_t>(chunk, t.numel - at));
         c.second = uint8_t(t.second_moment);
         c.bf16 = t.value_dtype == MUON_BF16;
         table.push_back(c);
@@ -459,10 +485,8 @@ muon_status muon_state8_plan_create(muon_ctx* ctx, const muon_state8_tensor* ten
     }
     if (overlapping(spans))
       return fail(ctx, MUON_ERR_INVALID_ARG, "two tensors of the plan overlap");
-    if (int64_t(table.size()) > kMaxChunks)
-      return fail(ctx, MUON_ERR_UNSUPPORTED, "more elements than one launch covers");
     plan->buckets.emplace_back();
-    plan->buckets[0].chunks = int64_t(table.size());
+    plan->buckets[0].chunks = table.size();
     return finish_plan(ctx, plan, table, out);
   });
 }
@@ -471,15 +495,16 @@ static muon_status state8_run(muon_plan* plan, bool pack, void* stream) {
   muon_status s = check_plan(plan, PLAN_STATE8);
   if (s != MUON_OK) return s;
   muon_ctx* ctx = plan->ctx;
-  if (plan->buckets[0].chunks == 0) return MUON_OK;
+  const PlanBucket& b = plan->buckets[0];
+  if (b.chunks == 0) return MUON_OK;
   DeviceGuard guard(plan->device);
   CUDA_TRY(ctx, guard.err);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   ctx->last_stream = st;
   CUDA_TRY(ctx, cudaGetLastError());
   ProfScope ps(ctx, MUON_K_OTHER, st);
-  const dim3 grid{unsigned(plan->buckets[0].chunks)};
   const Q8Chunk* t = static_cast<const Q8Chunk*>(plan->table);
+  const dim3 grid{unsigned(b.chunks)};
   const int* flags = ctx->dflags;
   CUDA_TRY(ctx, pack ? launch_pdl(state8_kernel<true>, grid, dim3(ST_THREADS), size_t(0), st, t, flags)
                      : launch_pdl(state8_kernel<false>, grid, dim3(ST_THREADS), size_t(0), st, t, flags));
