@@ -47,8 +47,8 @@ constexpr int ST_WARPS = ST_THREADS / 32;
 constexpr int ADAM8_CTAS = 4;             // resident thread blocks per SM
 constexpr int ADAM8_SMEM = 55 * 1024;     // of shared memory each
 constexpr int STATE8_BLOCKS = 4;          // per warp
-constexpr int NORM_CHUNK = 8192;
-constexpr int NORM_CTAS = 8;              // resident thread blocks per SM
+constexpr int NORM_BYTES = 32768;         // of gradients in a chunk
+constexpr int NORM_CTAS = 4;              // resident thread blocks per SM
 constexpr int MAX_SLOTS = 480;          // tensors of one launch: their gradient pointers are a kernel
                                         // parameter (3840 B), so rebinding gradients touches no
                                         // device memory that a launch in flight could be reading
@@ -850,7 +850,7 @@ __global__ void __launch_bounds__(ST_THREADS) state8_kernel(const Q8Chunk* __res
 struct alignas(16) NormChunk {
   int64_t base;            // first element's index in its tensor
   uint16_t slot;
-  uint16_t count;          // 1 .. NORM_CHUNK
+  uint16_t count;          // elements
   uint32_t bf16;
 };
 static_assert(sizeof(NormChunk) == 16, "");
@@ -860,14 +860,11 @@ static_assert(sizeof(NormChunk) == 16, "");
 // are formed in 64 bits.
 __device__ __forceinline__ double squares8(const float (&x)[8]) {
   float s = 0.f;
-  uint32_t any = 0;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    s = fmaf(x[k], x[k], s);
-    any |= __float_as_uint(x[k]) << 1;
-  }
+  for (int k = 0; k < 8; ++k) s = fmaf(x[k], x[k], s);
   if (s > 1e-25f && s < 1e37f) return static_cast<double>(s);
-  if (any == 0) return 0.0;
+  // all zero, as the rows of an embedding that no token touched?
+  if (max_abs8(x) == 0.f) return 0.0;
   double d = 0.0;
 #pragma unroll
   for (int k = 0; k < 8; ++k) d = fma(static_cast<double>(x[k]), static_cast<double>(x[k]), d);
@@ -904,33 +901,30 @@ struct NormOut {
 // loaded at once.
 template <bool BF16>
 __device__ __forceinline__ double square_chunk(const char* g, int count) {
-  constexpr int N = BF16 ? 8 : 4, U = 8, V = NORM_CHUNK / N / ST_THREADS;    // elements and vectors of a thread
-  double acc = 0.0;
-  if (count == NORM_CHUNK && aligned(g, 16)) {
+  constexpr int V = NORM_BYTES / 16 / ST_THREADS;         // vectors of a thread, 8 of them in flight at once:
+  double acc = 0.0;                                       // 4 left bf16 gradients at 79 % of the copy's bandwidth
+  if (count == NORM_BYTES / (BF16 ? 2 : 4) && aligned(g, 16)) {
     const uint4* p = reinterpret_cast<const uint4*>(g) + threadIdx.x;
+    uint4 raw[V];
 #pragma unroll
-    for (int i = 0; i < V; i += U) {
-      uint4 raw[U];
+    for (int u = 0; u < V; ++u) raw[u] = p[u * ST_THREADS];
 #pragma unroll
-      for (int u = 0; u < U && i + u < V; ++u) raw[u] = p[(i + u) * ST_THREADS];
-#pragma unroll
-      for (int u = 0; u < U && i + u < V; u += BF16 ? 1 : 2) {
-        float x[8];
-        if (BF16) {
-          const float2 a = unpack_bf16x2(raw[u].x), b = unpack_bf16x2(raw[u].y), c = unpack_bf16x2(raw[u].z),
-                       d = unpack_bf16x2(raw[u].w);
-          x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y; x[4] = c.x; x[5] = c.y; x[6] = d.x; x[7] = d.y;
-        } else {
-          const uint4 w = raw[u], z = raw[u + 1 < U ? u + 1 : u];
-          x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y); x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
-          x[4] = __uint_as_float(z.x); x[5] = __uint_as_float(z.y); x[6] = __uint_as_float(z.z); x[7] = __uint_as_float(z.w);
-        }
-        acc += squares8(x);
+    for (int u = 0; u < V; u += BF16 ? 1 : 2) {
+      float x[8];
+      if (BF16) {
+        const float2 a = unpack_bf16x2(raw[u].x), b = unpack_bf16x2(raw[u].y), c = unpack_bf16x2(raw[u].z),
+                     d = unpack_bf16x2(raw[u].w);
+        x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y; x[4] = c.x; x[5] = c.y; x[6] = d.x; x[7] = d.y;
+      } else {
+        const uint4 w = raw[u], z = raw[u + 1];
+        x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y); x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
+        x[4] = __uint_as_float(z.x); x[5] = __uint_as_float(z.y); x[6] = __uint_as_float(z.z); x[7] = __uint_as_float(z.w);
       }
+      acc += squares8(x);
     }
     return acc;
   }
-  for (int b = (threadIdx.x >> 5) * Q_BLOCK; b < count; b += ST_THREADS * 8) {
+  for (int b = (threadIdx.x >> 5) * Q_BLOCK; b < count; b += ST_WARPS * Q_BLOCK) {
     float x[8];
     const char* block = g + b * (BF16 ? 2 : 4);
     load8<BF16>(block, threadIdx.x & 31, count - b >= Q_BLOCK && aligned(block, 16), count - b, x);
@@ -940,7 +934,7 @@ __device__ __forceinline__ double square_chunk(const char* g, int count) {
 }
 
 // Thread block b takes chunks b, b + gridDim.x, ...
-__global__ void __launch_bounds__(ST_THREADS)
+__global__ void __launch_bounds__(ST_THREADS, NORM_CTAS)
     grad_norm_kernel(const NormChunk* __restrict__ chunks, unsigned nchunks, const __grid_constant__ GradPtrs grads,
                      const NormOut o) {
   __shared__ double red[ST_WARPS];
@@ -956,19 +950,21 @@ __global__ void __launch_bounds__(ST_THREADS)
     if (c < nchunks) ch = chunks[c];
     acc += now.bf16 ? square_chunk<true>(g, now.count) : square_chunk<false>(g, now.count);
   }
-  const double mine = block_sum_f64(acc, red);
-  if (threadIdx.x == 0) {
-    if (o.total > 0) o.partials[o.first + blockIdx.x] = mine;
+  double sum = block_sum_f64(acc, red);
+  if (o.total > 1) {
+    if (threadIdx.x == 0) {
+      o.partials[o.first + blockIdx.x] = sum;
+      __threadfence();
+      // wraps to 0 when every block has come by
+      last = atomicInc(o.counter, o.total - 1) == o.total - 1;
+    }
+    __syncthreads();
+    if (!last) return;
     __threadfence();
-    // wraps to 0 when every block has come by
-    last = o.total == 0 || atomicInc(o.counter, o.total - 1) == o.total - 1;
+    sum = 0.0;
+    for (unsigned int i = threadIdx.x; i < o.total; i += ST_THREADS) sum += __ldcg(o.partials + i);
+    sum = block_sum_f64(sum, red);
   }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  double sum = 0.0;
-  for (unsigned int i = threadIdx.x; i < o.total; i += ST_THREADS) sum += __ldcg(o.partials + i);
-  sum = block_sum_f64(sum, red);
   if (threadIdx.x == 0) {
     const float norm = static_cast<float>(sqrt(sum));
     o.out[0] = norm;

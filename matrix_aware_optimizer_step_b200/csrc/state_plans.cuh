@@ -373,9 +373,9 @@ muon_status muon_grad_norm_plan_create(muon_ctx* ctx, const muon_grad_tensor* te
       b.first = table.size();
       for (size_t k = 0; k < b.tensors.size(); ++k) {
         const muon_grad_tensor& t = tensors[b.tensors[k]];
-        for (int64_t at = 0; at < t.numel; at += NORM_CHUNK)
-          table.push_back({at, uint16_t(k), uint16_t(std::min<int64_t>(NORM_CHUNK, t.numel - at)),
-                           t.grad_dtype == MUON_BF16 ? 1u : 0u});
+        const int64_t chunk = NORM_BYTES / dtype_size(t.grad_dtype);
+        for (int64_t at = 0; at < t.numel; at += chunk)
+          table.push_back({at, uint16_t(k), uint16_t(std::min(chunk, t.numel - at)), t.grad_dtype == MUON_BF16 ? 1u : 0u});
       }
       b.chunks = table.size() - b.first;
       plan->norm_grid.push_back(unsigned(std::min(b.chunks, most)));

@@ -49,9 +49,7 @@ def _check(t, what: str, device: int, numel: Optional[int] = None, dtypes=None):
         raise TypeError(f"{what}: unsupported dtype {t.dtype}")
 
 
-def _scalar_ptr(t, what: str, device: int, dtype) -> Optional[int]:
-    if t is None:
-        return None
+def _scalar_ptr(t, what: str, device: int, dtype) -> int:
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.numel() < 1:
         raise TypeError(f"{what}: a {dtype} tensor of one element is wanted")
     if not t.is_cuda or t.device.index != device:
@@ -60,6 +58,14 @@ def _scalar_ptr(t, what: str, device: int, dtype) -> Optional[int]:
 
 
 _FLOATS = (torch.float32, torch.bfloat16)
+
+
+def _current_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# the same pointer without building a Stream object: a third of a small call's host time
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 
 
 class _Plan:
@@ -80,18 +86,16 @@ class _Plan:
             self._h = ctypes.c_void_p()
         self._ctx._check(st, fn.__name__)
 
-    def _call(self, fn, *args):
-        st = fn(self._h, *args)
-        if st != MUON_OK:
-            if not self._h:
-                raise MuonError(st, f"{fn.__name__}: the plan is closed")
-            if not self._ctx._ctx:
-                raise MuonError(st, f"{fn.__name__}: the context is closed")
-            self._ctx._check(st, fn.__name__)
+    def _failed(self, st, what):
+        if not self._h:
+            raise MuonError(st, f"{what}: the plan is closed")
+        if not self._ctx._ctx:
+            raise MuonError(st, f"{what}: the context is closed")
+        self._ctx._check(st, what)
 
     def _stream(self, stream) -> int:
         if stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
+            return _current_stream(self.device)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
     def close(self):
@@ -124,7 +128,9 @@ class _GradPlan(_Plan):
         for g, (n, dt) in zip(grads, self._like):
             _check(g, "bind_grads", self.device, n, (dt,))
         arr = (ctypes.c_void_p * max(1, len(grads)))(*[g.data_ptr() for g in grads])
-        self._call(self._lib.muon_plan_bind_grads, arr, len(grads))
+        st = self._lib.muon_plan_bind_grads(self._h, arr, len(grads))
+        if st != MUON_OK:
+            self._failed(st, "muon_plan_bind_grads")
         self._grads = grads
 
 
@@ -165,6 +171,7 @@ class AdamwPlan(_GradPlan):
                     raise TypeError("adamw_plan: a bf16 copy goes with an fp32 parameter")
                 a.param_copy = copies[i].data_ptr()
         self._default = default_adamw_plan_hparams()
+        self._step = self._lib.muon_adamw_plan_step
         self._create(self._lib.muon_adamw_plan_create, arr, n, self.state_bits)
 
     def step(self, step, hp: Optional[AdamwPlanHparams] = None, lr=None, grad_scale=None, seed: Optional[int] = None,
@@ -177,16 +184,21 @@ class AdamwPlan(_GradPlan):
         None rounds 8-bit codes and bf16 parameters to nearest, an int in
         [0, 2^32) stochastically, by numbers hashed from it, the step, the
         tensor's place in the list and the element."""
-        step_ptr = None
+        step_ptr = lr_ptr = scale_ptr = None
         if isinstance(step, torch.Tensor):
             step_ptr = _scalar_ptr(step, "step", self.device, torch.int64)
             step = 0
+        if lr is not None:
+            lr_ptr = _scalar_ptr(lr, "lr", self.device, torch.float32)
+        if grad_scale is not None:
+            scale_ptr = _scalar_ptr(grad_scale, "grad_scale", self.device, torch.float32)
         if seed is not None and not 0 <= seed < 1 << 32:
             raise ValueError("seed must lie in [0, 2^32)")
-        self._call(self._lib.muon_adamw_plan_step, ctypes.byref(hp if hp is not None else self._default), int(step),
-                   step_ptr, _scalar_ptr(lr, "lr", self.device, torch.float32),
-                   _scalar_ptr(grad_scale, "grad_scale", self.device, torch.float32),
-                   0 if seed is None else 1, seed or 0, self._stream(stream))
+        st = self._step(self._h, self._default if hp is None else hp, int(step), step_ptr, lr_ptr, scale_ptr,
+                        seed is not None, seed or 0,
+                        _current_stream(self.device) if stream is None else self._stream(stream))
+        if st != MUON_OK:
+            self._failed(st, "muon_adamw_plan_step")
 
 
 class GradNormPlan(_GradPlan):
@@ -202,9 +214,10 @@ class GradNormPlan(_GradPlan):
             a.numel, a.grad_dtype, a.grad = g.numel(), _dtype_code(g), g.data_ptr()
         self._create(self._lib.muon_grad_norm_plan_create, arr, len(grads))
         n = ctypes.c_size_t()
-        self._call(self._lib.muon_grad_norm_out_bytes, ctypes.byref(n))
+        self._lib.muon_grad_norm_out_bytes(self._h, ctypes.byref(n))
         self._floats = n.value // 4
-        self._out = None
+        self._result = None
+        self._run = self._lib.muon_grad_norm_run
 
     def new_output(self):
         """A result buffer: its first two elements are the result, the rest is
@@ -217,14 +230,16 @@ class GradNormPlan(_GradPlan):
         when the norm is not finite.  `out`: a buffer of new_output(), the
         plan's own by default, which the next run overwrites."""
         if out is None:
-            if self._out is None:
-                self._out = self.new_output()
-                self._result = self._out[:2]
-            out, result = self._out, self._result
+            if self._result is None:
+                self._result = self.new_output()[:2]
+                self._result_ptr = self._result.data_ptr()
+            result, ptr = self._result, self._result_ptr
         else:
             _check(out, "out", self.device, self._floats, (torch.float32,))
-            result = out[:2]
-        self._call(self._lib.muon_grad_norm_run, float(max_norm), out.data_ptr(), self._stream(stream))
+            result, ptr = out[:2], out.data_ptr()
+        st = self._run(self._h, max_norm, ptr, _current_stream(self.device) if stream is None else self._stream(stream))
+        if st != MUON_OK:
+            self._failed(st, "muon_grad_norm_run")
         return result
 
 
@@ -250,8 +265,12 @@ class State8Plan(_Plan):
 
     def pack(self, stream=None):
         """Values to codes and scales, rounded to nearest."""
-        self._call(self._lib.muon_state8_pack, self._stream(stream))
+        st = self._lib.muon_state8_pack(self._h, self._stream(stream))
+        if st != MUON_OK:
+            self._failed(st, "muon_state8_pack")
 
     def unpack(self, stream=None):
         """Codes and scales to the values they stand for."""
-        self._call(self._lib.muon_state8_unpack, self._stream(stream))
+        st = self._lib.muon_state8_unpack(self._h, self._stream(stream))
+        if st != MUON_OK:
+            self._failed(st, "muon_state8_unpack")
