@@ -855,16 +855,19 @@ struct alignas(16) NormChunk {
 };
 static_assert(sizeof(NormChunk) == 16, "");
 
-// Sum of squares of up to 8 elements in 64 bits.  fp32 holds it to 2^-22 when
-// it lies well inside fp32's range; else (tiny or huge gradients) the squares
-// are formed in 64 bits.
-__device__ __forceinline__ double squares8(const float (&x)[8]) {
+// Sum of squares of up to 8 elements.  fp32 holds it to 2^-22 when it lies well
+// inside fp32's range; if not (tiny or huge gradients, but not all zeros, as
+// the rows of an embedding that no token touched have) `bad` is set and the
+// squares have to be formed in 64 bits.
+__device__ __forceinline__ float squares8(const float (&x)[8], bool& bad) {
   float s = 0.f;
 #pragma unroll
   for (int k = 0; k < 8; ++k) s = fmaf(x[k], x[k], s);
-  if (s > 1e-25f && s < 1e37f) return static_cast<double>(s);
-  // all zero, as the rows of an embedding that no token touched?
-  if (max_abs8(x) == 0.f) return 0.0;
+  bad |= !(s > 1e-25f && s < 1e37f) && max_abs8(x) != 0.f;
+  return s;
+}
+
+__device__ __forceinline__ double squares8_wide(const float (&x)[8]) {
   double d = 0.0;
 #pragma unroll
   for (int k = 0; k < 8; ++k) d = fma(static_cast<double>(x[k]), static_cast<double>(x[k]), d);
@@ -908,19 +911,31 @@ __device__ __forceinline__ double square_chunk(const char* g, int count) {
     uint4 raw[V];
 #pragma unroll
     for (int u = 0; u < V; ++u) raw[u] = p[u * ST_THREADS];
-#pragma unroll
-    for (int u = 0; u < V; u += BF16 ? 1 : 2) {
-      float x[8];
+    auto eight = [](const uint4& w, const uint4& z, float (&x)[8]) {
       if (BF16) {
-        const float2 a = unpack_bf16x2(raw[u].x), b = unpack_bf16x2(raw[u].y), c = unpack_bf16x2(raw[u].z),
-                     d = unpack_bf16x2(raw[u].w);
+        const float2 a = unpack_bf16x2(w.x), b = unpack_bf16x2(w.y), c = unpack_bf16x2(w.z), d = unpack_bf16x2(w.w);
         x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y; x[4] = c.x; x[5] = c.y; x[6] = d.x; x[7] = d.y;
       } else {
-        const uint4 w = raw[u], z = raw[u + 1];
         x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y); x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
         x[4] = __uint_as_float(z.x); x[5] = __uint_as_float(z.y); x[6] = __uint_as_float(z.z); x[7] = __uint_as_float(z.w);
       }
-      acc += squares8(x);
+    };
+    constexpr int S = BF16 ? 1 : 2;      // vectors of 8 elements
+    bool bad = false;
+#pragma unroll
+    for (int u = 0; u < V; u += S) {
+      float x[8];
+      eight(raw[u], raw[u + S - 1], x);
+      acc += squares8(x, bad);
+    }
+    if (bad) {
+      acc = 0.0;
+#pragma unroll 1
+      for (int u = 0; u < V; u += S) {
+        float x[8];
+        eight(p[u * ST_THREADS], p[(u + S - 1) * ST_THREADS], x);
+        acc += squares8_wide(x);
+      }
     }
     return acc;
   }
@@ -928,7 +943,9 @@ __device__ __forceinline__ double square_chunk(const char* g, int count) {
     float x[8];
     const char* block = g + b * (BF16 ? 2 : 4);
     load8<BF16>(block, threadIdx.x & 31, count - b >= Q_BLOCK && aligned(block, 16), count - b, x);
-    acc += squares8(x);
+    bool bad = false;
+    const float s = squares8(x, bad);
+    acc += bad ? squares8_wide(x) : static_cast<double>(s);
   }
   return acc;
 }
