@@ -7,28 +7,40 @@ list of param groups, each with ``use_muon``; Muon groups take ``lr``,
 take ``lr``, ``betas``, ``eps``, ``weight_decay``.  Which parameters are
 "hidden" is the caller's choice, as the README says.
 
+AdamW groups take three keys more: ``state_bits`` (32, or 8 for moments in
+8 bits), ``max_grad_norm`` (clip the 2-norm over the group's gradients; a step
+whose norm is not finite changes nothing) and ``seed`` (round 8-bit codes and
+bf16 parameters stochastically).
+
 This file only keeps optimizer state tensors and hands pointers to the
 library: every update runs in libmuon_b200.so.
 """
 
 from __future__ import annotations
 
+from itertools import chain
 from typing import Iterable
 
 import torch
 
-from .binding import MuonContext, default_adamw_hparams, default_hparams
+from .binding import MuonContext, default_adamw_hparams, default_adamw_plan_hparams, default_hparams
+from .plans import state8_zeros
 
 MUON_DEFAULTS = dict(lr=0.02, weight_decay=0.01, momentum=0.95, nesterov=True, ns_steps=5,
                      scale_mode="original")
-ADAMW_DEFAULTS = dict(lr=3e-4, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.01)
+ADAMW_DEFAULTS = dict(lr=3e-4, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.01, state_bits=32,
+                      max_grad_norm=None, seed=None)
 
 
 class MuonWithAuxAdam(torch.optim.Optimizer):
     """Muon for groups with use_muon=True (parameters of two or more
     dimensions, stepped as rows x prod(other dims) matrices), AdamW for the
-    rest.  Parameters must be contiguous fp32 CUDA tensors on one device;
-    gradients fp32 or bf16.
+    rest.  Parameters must be contiguous CUDA tensors on one device, fp32, or
+    bf16 in AdamW groups; gradients fp32 or bf16.
+
+    A group's state_bits may be changed between steps, after loading a
+    checkpoint for instance: its moments are converted at the next step.
+    A step skipped for a norm that is not finite still counts.
 
     Device-side failures (a bounded wait inside a kernel that gave up) are
     flagged on the GPU; from then on the library leaves every parameter and
@@ -45,18 +57,27 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
             base = MUON_DEFAULTS if g["use_muon"] else ADAMW_DEFAULTS
             for k, v in base.items():
                 g.setdefault(k, v)
+            if not g["use_muon"]:
+                if g["state_bits"] not in (8, 32):
+                    raise ValueError("state_bits must be 8 or 32")
+                if g["max_grad_norm"] is not None and not g["max_grad_norm"] >= 0:
+                    raise ValueError("max_grad_norm must be >= 0")
+                if g["seed"] is not None and not 0 <= g["seed"] < 1 << 32:
+                    raise ValueError("seed must lie in [0, 2^32)")
             groups.append(g)
         super().__init__(groups, dict())
         for g in self.param_groups:
             for p in g["params"]:
-                if not p.is_cuda or p.dtype != torch.float32 or not p.is_contiguous():
-                    raise ValueError("parameters must be contiguous fp32 CUDA tensors")
+                if not p.is_cuda or not p.is_contiguous() or not (
+                        p.dtype == torch.float32 or p.dtype == torch.bfloat16 and not g["use_muon"]):
+                    raise ValueError("parameters must be contiguous fp32 CUDA tensors (bf16 too in AdamW groups)")
                 if g["use_muon"] and p.dim() < 2:
                     raise ValueError("Muon parameters need two or more dimensions")
         first = next(p for g in self.param_groups for p in g["params"])
         self.ctx = MuonContext(first.device.index if device is None else device)
         self.check_every = int(check_every)
         self._steps = 0
+        self._plans = {}       # what the AdamW groups' plans were built over, and the plans
 
     def check(self):
         """Synchronise and raise MuonError if a device-side wait gave up since
@@ -69,12 +90,15 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
-        for g in self.param_groups:
+        for i, g in enumerate(self.param_groups):
             params = [p for p in g["params"] if p.grad is not None]
             if not params:
                 continue
             if g["use_muon"]:
                 self._muon(g, params)
+            elif (g.get("state_bits", 32) == 8 or g.get("max_grad_norm") is not None or g.get("seed") is not None
+                  or any(p.dtype != torch.float32 or "exp_avg_scale" in self.state[p] for p in params)):
+                self._adamw_planned(i, g, params)
             else:
                 self._adamw(g, params)
         self._steps += 1
@@ -116,3 +140,89 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
             self.ctx.adamw_step([p.view(-1) for p in ps], [p.grad.reshape(-1).contiguous() for p in ps],
                                 [self.state[p]["exp_avg"].view(-1) for p in ps],
                                 [self.state[p]["exp_avg_sq"].view(-1) for p in ps], step, hp)
+
+    # -- AdamW through plans ------------------------------------------------
+    def _moments(self, params, bits):
+        """Zero moments where there are none; those of the other form are
+        converted."""
+        convert = []
+        for p in params:
+            st = self.state[p]
+            if "step" not in st:
+                st["step"] = 0
+                st.update(state8_zeros(p) if bits == 8 else dict(
+                    exp_avg=torch.zeros_like(p, dtype=torch.float32), exp_avg_sq=torch.zeros_like(p, dtype=torch.float32)))
+            elif ("exp_avg_scale" in st) != (bits == 8):
+                convert.append(p)
+        if not convert:
+            return
+        wide, codes, scales = [], [], []
+        for p in convert:
+            st = self.state[p]
+            full = {k: st[k] if bits == 8 else torch.empty_like(p, dtype=torch.float32) for k in ("exp_avg", "exp_avg_sq")}
+            small = state8_zeros(p) if bits == 8 else {k: st[k] for k in ("exp_avg", "exp_avg_sq", "exp_avg_scale",
+                                                                         "exp_avg_sq_scale")}
+            for k in ("exp_avg", "exp_avg_sq"):
+                wide.append(full[k].contiguous())
+                codes.append(small[k])
+                scales.append(small[k + "_scale"])
+            st.pop("exp_avg_scale", None)
+            st.pop("exp_avg_sq_scale", None)
+            st.update(small if bits == 8 else full)
+        plan = self.ctx.state8_plan(wide, codes, scales)
+        plan.pack() if bits == 8 else plan.unpack()
+        plan.close()
+
+    def _plan(self, key, tensors, grads, build):
+        """The plan of `key`, rebuilt when its tensors or the gradients' types
+        changed, with these gradients."""
+        at = [t.data_ptr() for t in tensors] + [(g.dtype, g.numel()) for g in grads]
+        ptrs = [g.data_ptr() for g in grads]
+        had = self._plans.get(key)
+        if had is None or had[0] != at:
+            if len(self._plans) > 64:      # parameters that come and go
+                self._plans.clear()
+            had = self._plans[key] = [at, ptrs, build()]
+        elif had[1] != ptrs:
+            had[2].bind_grads(grads)
+            had[1] = ptrs
+        had[2].forget_grads()      # a gradient freed by zero_grad is not kept to the next step
+        return had[2]
+
+    def _adamw_planned(self, index, g, params):
+        bits, clip = int(g.get("state_bits", 32)), g.get("max_grad_norm")
+        self._moments(params, bits)
+        b1, b2 = g["betas"]
+        hp = default_adamw_plan_hparams(lr=g["lr"], beta1=b1, beta2=b2, eps=g["eps"], weight_decay=g["weight_decay"])
+        grads = {p: p.grad.reshape(-1).contiguous() for p in params}
+        factor = None
+        if clip is not None:
+            gs = list(grads.values())
+            norm = self._plan((index, "norm", tuple(map(id, params))), [], gs, lambda: self.ctx.grad_norm_plan(gs))
+            factor = norm.run(float(clip))[1:]
+        by_step = {}
+        for p in params:
+            self.state[p]["step"] += 1
+            by_step.setdefault(self.state[p]["step"], []).append(p)
+        names = ["exp_avg", "exp_avg_sq"] + (["exp_avg_scale", "exp_avg_sq_scale"] if bits == 8 else [])
+        for step, ps in by_step.items():
+            lists = [[p.detach().view(-1) for p in ps]] + [[self.state[p][k].view(-1) for p in ps] for k in names]
+            gs = [grads[p] for p in ps]
+            plan = self._plan((index, bits, tuple(map(id, ps))), list(chain(*lists)), gs,
+                              lambda: self.ctx.adamw_plan(lists[0], gs, *lists[1:]))
+            plan.step(step, hp, grad_scale=factor, seed=g.get("seed"))
+
+    def load_state_dict(self, state_dict):
+        """As torch.optim.Optimizer's, except that 8-bit codes stay what they
+        are and every other state tensor becomes fp32 (the base class casts
+        state to the parameter's type, which would round the moments and
+        scales of bf16 parameters and turn codes into numbers)."""
+        super().load_state_dict(state_dict)
+        saved = chain.from_iterable(g["params"] for g in state_dict["param_groups"])
+        own = chain.from_iterable(g["params"] for g in self.param_groups)
+        for k, p in zip(saved, own):
+            for name, t in state_dict["state"].get(k, {}).items():
+                if isinstance(t, torch.Tensor):
+                    dtype = torch.float32 if t.is_floating_point() else t.dtype
+                    self.state[p][name] = t.detach().to(device=p.device, dtype=dtype, copy=True).contiguous()
+        self._plans.clear()

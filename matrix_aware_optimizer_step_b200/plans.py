@@ -133,6 +133,12 @@ class _GradPlan(_Plan):
             self._failed(st, "muon_plan_bind_grads")
         self._grads = grads
 
+    def forget_grads(self):
+        """Stop holding references to the bound gradients.  The plan goes on
+        using their addresses: the caller keeps them alive for each call, or
+        binds others first."""
+        self._grads = None
+
 
 class AdamwPlan(_GradPlan):
     """AdamW over a list of tensors; built by MuonContext.adamw_plan."""
