@@ -420,7 +420,7 @@ MUON_API muon_status muon_state8_pack(muon_plan* plan, void* stream);
 MUON_API muon_status muon_state8_unpack(muon_plan* plan, void* stream);
 
 /* No counterpart on the pages (resource management).  Free a plan of any
- * kind (synchronises the device).  Graphs that captured its calls must not
+ * kind, waiting for work that may use it.  Graphs that captured its calls must not
  * be replayed afterwards.  Plans outlive their context only to be destroyed:
  * other calls on them then return MUON_ERR_INVALID_ARG.  NULL: no effect. */
 MUON_API void muon_plan_destroy(muon_plan* plan);

@@ -1481,7 +1481,10 @@ void muon_destroy(muon_ctx* ctx) {
       cudaEventDestroy(pr.second);
     }
   for (auto e : ctx->prof_pool) cudaEventDestroy(e);
-  for (muon_plan* p : ctx->plans) p->ctx = nullptr;
+  {
+    std::lock_guard<std::mutex> lock(g_plans_mutex);
+    for (muon_plan* p : ctx->plans) p->ctx = nullptr;
+  }
   delete ctx;
 }
 

@@ -55,7 +55,10 @@ struct DeviceGuard {
   }
 };
 
-constexpr int64_t kMaxNumel = int64_t(1) << 40;
+constexpr int64_t kMaxNumel = int64_t(1) << 38;   // no GPU holds more
+
+// Plans may be freed by a garbage collector's thread.
+std::mutex g_plans_mutex;
 
 bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -101,6 +104,7 @@ muon_status finish_plan(muon_ctx* ctx, muon_plan* plan, const std::vector<T>& ta
       return fail(ctx, MUON_ERR_CUDA, "table upload failed: %s", cudaGetErrorString(e));
     }
   }
+  std::lock_guard<std::mutex> lock(g_plans_mutex);
   ctx->plans.push_back(plan);
   *out = plan;
   return MUON_OK;
@@ -416,8 +420,12 @@ muon_status muon_grad_norm_run(muon_plan* plan, double max_norm, float* out, voi
   for (size_t k = 0; k < plan->buckets.size(); ++k) {
     const PlanBucket& b = plan->buckets[k];
     fill_grads(plan, b, g);
-    CUDA_TRY(ctx, launch_pdl(grad_norm_kernel, dim3(plan->norm_grid[k]), dim3(ST_THREADS), size_t(0), st,
-                             static_cast<const NormChunk*>(plan->table) + b.first, unsigned(b.chunks), g, o));
+    const cudaError_t e = launch_pdl(grad_norm_kernel, dim3(plan->norm_grid[k]), dim3(ST_THREADS), size_t(0), st,
+                                     static_cast<const NormChunk*>(plan->table) + b.first, unsigned(b.chunks), g, o);
+    if (e != cudaSuccess) {      // launches that did go out must not leave a count for the next run
+      cudaMemsetAsync(o.counter, 0, sizeof(unsigned int), st);
+      return fail(ctx, MUON_ERR_CUDA, "grad_norm launch failed: %s", cudaGetErrorString(e));
+    }
     ctx->launches++;
     o.first += plan->norm_grid[k];
   }
@@ -518,14 +526,21 @@ muon_status muon_state8_unpack(muon_plan* plan, void* stream) { return state8_ru
 
 void muon_plan_destroy(muon_plan* plan) {
   if (!plan) return;
-  if (plan->ctx) {
-    auto& v = plan->ctx->plans;
-    v.erase(std::remove(v.begin(), v.end(), plan), v.end());
+  {
+    std::lock_guard<std::mutex> lock(g_plans_mutex);
+    if (plan->ctx) {
+      auto& v = plan->ctx->plans;
+      v.erase(std::remove(v.begin(), v.end(), plan), v.end());
+    }
   }
   if (plan->table) {
+    // cudaFree waits for work that may read the table.  Another stream may be
+    // capturing just now: freeing must not end its capture.
     DeviceGuard guard(plan->device);
-    cudaDeviceSynchronize();
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    const bool relaxed = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
     cudaFree(plan->table);
+    if (relaxed) cudaThreadExchangeStreamCaptureMode(&mode);
   }
   delete plan;
 }

@@ -222,12 +222,14 @@ class GradNormPlan(_GradPlan):
         n = ctypes.c_size_t()
         self._lib.muon_grad_norm_out_bytes(self._h, ctypes.byref(n))
         self._floats = n.value // 4
-        self._result = None
+        self._result = self.new_output()[:2]
+        self._result_ptr = self._result.data_ptr()
+        torch.cuda.current_stream(self.device).synchronize()      # zeroed, whichever stream runs first
         self._run = self._lib.muon_grad_norm_run
 
     def new_output(self):
-        """A result buffer: its first two elements are the result, the rest is
-        the call's workspace.  Runs that may overlap in time (other streams,
+        """A result buffer, zeroed on the current stream: its first two
+        elements are the result, the rest is the call's workspace.  Runs that may overlap in time (other streams,
         captured graphs that replay side by side) need one each."""
         return torch.zeros(self._floats, dtype=torch.float32, device=torch.device("cuda", self.device))
 
@@ -236,9 +238,6 @@ class GradNormPlan(_GradPlan):
         when the norm is not finite.  `out`: a buffer of new_output(), the
         plan's own by default, which the next run overwrites."""
         if out is None:
-            if self._result is None:
-                self._result = self.new_output()[:2]
-                self._result_ptr = self._result.data_ptr()
             result, ptr = self._result, self._result_ptr
         else:
             _check(out, "out", self.device, self._floats, (torch.float32,))

@@ -758,3 +758,100 @@ def test_one_tensor_past_2_to_31_elements(ctx, mx):
     ctx.state8_plan([values], [m], [ms]).unpack()
     torch.cuda.synchronize()
     assert np.array_equal(f32(values[first:]), ref.round_bf16(ref.decode_m(c, s)))
+
+
+@gpu
+@pytest.mark.parametrize("mag", [1e-9, 1e-12, 1e-14, 1e-17, 1e-20, 1e12])
+@pytest.mark.parametrize("eps", [1e-8, 1e-20])
+def test_adamw8_over_the_range_of_gradients(ctx, mx, mag, eps):
+    """Blocks either side of the range that the fast path takes, subnormal
+    second moments among them, and an eps that its flushes would reach: codes
+    bit for bit, parameters within their bound."""
+    T = Tensors([4099], 30, False, False, True, zero=True)
+    plan, rng = T.plan(ctx), np.random.default_rng(31)
+    hp = mx.default_adamw_plan_hparams(eps=eps)
+    for t in (1, 2):
+        g = (rng.standard_normal(4099) * np.exp(3 * rng.standard_normal(4099)) * mag).astype(np.float32)
+        T.tg[0].copy_(torch.from_numpy(g))
+        plan.step(t, hp)
+        torch.cuda.synchronize()
+        m32, v32 = ref.moments(T.m[0], T.v[0], g, 0.9, 0.95)
+        (c, s), (d, q) = ref.encode_m(m32), ref.encode_v(v32)
+        assert np.array_equal(T.tm[0].cpu().numpy(), c) and np.array_equal(T.tv[0].cpu().numpy(), d)
+        assert np.array_equal(T.tms[0].cpu().numpy(), s) and np.array_equal(T.tvs[0].cpu().numpy(), q)
+        # the parameter from the fp32 moments (a subnormal v has few bits: its root is taken as it is)
+        r = np.sqrt(v32.astype(np.float64))
+        upd = 3e-4 / (1 - 0.9 ** t) * m32.astype(np.float64) / (r / math.sqrt(1 - 0.95 ** t) + eps)
+        p1 = T.p[0].astype(np.float64) * (1 - 3e-4 * 0.01) - upd
+        assert np.all(np.abs(f32(T.tp[0]) - p1) <= 4 * U * np.abs(T.p[0]) + 16 * U * np.abs(upd) + 1e-30)
+        T.m[0], T.v[0], T.p[0] = ref.decode_m(c, s), ref.decode_v(d, q), f32(T.tp[0])
+
+
+@gpu
+def test_two_graphs_of_one_plan_and_a_plan_freed_during_capture(ctx, mx):
+    T = Tensors([5000], 32, False, True, True)
+    R = Tensors([5000], 32, False, True, True)
+    plan, direct = T.plan(ctx), R.plan(ctx)
+    doomed = ctx.state8_plan([torch.zeros(300, device="cuda")], [torch.zeros(300, dtype=torch.int8, device="cuda")],
+                             [torch.zeros(2, device="cuda")])
+    gs = [T.new_grads()[0] for _ in range(2)]
+    bufs = [torch.from_numpy(g).cuda().bfloat16() for g in gs]
+    graphs = []
+    for t, b in enumerate(bufs, 1):
+        plan.bind_grads([b])
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            plan.step(t, seed=4)
+            if t == 1:
+                doomed.close()
+        graphs.append(graph)
+    plan.bind_grads(T.tg)          # captured calls keep their gradients
+    for t, b in enumerate(bufs, 1):
+        graphs[t - 1].replay()
+        direct.bind_grads([b])
+        direct.step(t, seed=4)
+    torch.cuda.synchronize()
+    for x, y in zip(T.tp + T.tm + T.tv + T.tms + T.tvs, R.tp + R.tm + R.tv + R.tms + R.tvs):
+        assert torch.equal(x, y)
+    del graphs
+
+
+@gpu
+def test_first_norm_on_another_stream(ctx):
+    for k in range(20):
+        g = torch.full((1000 * (k + 1),), 2.0, device="cuda")
+        torch.cuda.synchronize()
+        plan = ctx.grad_norm_plan([g])
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            r = plan.run(1.0)
+        side.synchronize()
+        assert abs(float(r[0]) - 2 * math.sqrt(g.numel())) <= 5 * U * float(r[0])
+
+
+@gpu
+def test_one_tensor_past_2_to_33_elements_hashes_its_high_word(ctx, mx):
+    """2^33 + 600 elements: pair numbers beyond 32 bits, the last blocks'
+    stochastic codes bit for bit."""
+    n = (1 << 33) + 600
+    if torch.cuda.mem_get_info()[0] < 7 * n:
+        pytest.skip("needs 60 GB of device memory")
+    p = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    g = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    m, v = torch.zeros(n, dtype=torch.int8, device="cuda"), torch.zeros(n, dtype=torch.uint8, device="cuda")
+    ms, vs = torch.zeros(-(-n // 256), device="cuda"), torch.zeros(-(-n // 256), device="cuda")
+    first = (1 << 33) - 512
+    x = grads_np(np.random.default_rng(33), n - first, True)
+    g[first:] = torch.from_numpy(x).cuda().bfloat16()
+    ctx.adamw_plan([p], [g], [m], [v], [ms], [vs]).step(1, seed=77)
+    torch.cuda.synchronize()
+    z = np.zeros(x.size, np.float32)
+    m32, v32 = ref.moments(z, z, x, 0.9, 0.95)
+    h, _ = ref.hashed(x.size, 77, 1, 0, first=first)
+    c, s = ref.encode_m(m32, ref.unit(ref.swap(h)))
+    d, q = ref.encode_v(v32, ref.unit(h))
+    assert np.array_equal(m[first:].cpu().numpy(), c) and np.array_equal(v[first:].cpu().numpy(), d)
+    assert np.array_equal(ms[first // 256:].cpu().numpy(), s) and np.array_equal(vs[first // 256:].cpu().numpy(), q)
+    del p, g, m, v
+    torch.cuda.empty_cache()
