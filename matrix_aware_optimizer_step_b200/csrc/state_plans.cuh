@@ -271,6 +271,9 @@ muon_status muon_adamw_plan_create(muon_ctx* ctx, const muon_plan_tensor* tensor
                                : (b.gbf16 ? Stage8<false, true>::blocks : Stage8<false, false>::blocks);
       b.blocks = s8 ? int(std::min<int64_t>(std::max<int64_t>(turn, 1), most)) : 1;
       const int64_t chunk = int64_t(b.blocks) * ST_WARPS * Q_BLOCK;
+      size_t more = 0;
+      for (int i : b.tensors) more += size_t(cdiv(tensors[i].numel, chunk));
+      table.reserve(table.size() + more);
       for (size_t k = 0; k < b.tensors.size(); ++k) {
         const muon_plan_tensor& t = tensors[b.tensors[k]];
         const int64_t es = s8 ? 1 : 4;
@@ -465,6 +468,10 @@ muon_status muon_state8_plan_create(muon_ctx* ctx, const muon_state8_tensor* ten
     std::vector<Span> spans;
     std::vector<Q8Chunk> table;
     constexpr int64_t chunk = int64_t(STATE8_BLOCKS) * ST_WARPS * Q_BLOCK;
+    size_t all = 0;
+    for (int i = 0; i < n; ++i)
+      if (tensors[i].numel > 0 && tensors[i].numel <= kMaxNumel) all += size_t(cdiv(tensors[i].numel, chunk));
+    table.reserve(all);
     for (int i = 0; i < n; ++i) {
       const muon_state8_tensor& t = tensors[i];
       if (t.numel < 0 || t.numel > kMaxNumel)

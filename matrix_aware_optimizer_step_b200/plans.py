@@ -15,11 +15,12 @@ zero moments of that form.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional, Sequence
 
 import torch
 
-from .binding import (MUON_OK, AdamwPlanHparams, GradTensor, MuonError, PlanTensor, State8Tensor, _dtype_code,
+from .binding import (MUON_BF16, MUON_F32, MUON_OK, AdamwPlanHparams, GradTensor, MuonError, PlanTensor, State8Tensor,
                       default_adamw_plan_hparams, load_library)
 
 STATE8_BLOCK = 256
@@ -41,12 +42,25 @@ def state8_zeros(like) -> dict:
 
 
 def _check(t, what: str, device: int, numel: Optional[int] = None, dtypes=None):
-    if not t.is_cuda or t.device.index != device or not t.is_contiguous():
+    if t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{what}: tensors must be contiguous CUDA tensors on device {device}")
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{what}: {t.numel()} elements where {numel} are wanted")
     if dtypes is not None and t.dtype not in dtypes:
         raise TypeError(f"{what}: unsupported dtype {t.dtype}")
+
+
+# the structs of the header, packed a list at a time (a ctypes field costs as
+# much as packing a struct)
+_PLAN_TENSOR, _GRAD_TENSOR, _STATE8_TENSOR = struct.Struct("@qii7Q"), struct.Struct("@qiiQ"), struct.Struct("@qii3Q")
+assert (_PLAN_TENSOR.size, _GRAD_TENSOR.size, _STATE8_TENSOR.size) == tuple(
+    map(ctypes.sizeof, (PlanTensor, GradTensor, State8Tensor)))
+_CODE = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}
+
+
+def _array(cls, packed):
+    """A ctypes array of `cls` from its packed elements."""
+    return (cls * max(1, len(packed))).from_buffer_copy(b"".join(packed) or bytes(ctypes.sizeof(cls)))
 
 
 def _scalar_ptr(t, what: str, device: int, dtype) -> int:
@@ -157,28 +171,27 @@ class AdamwPlan(_GradPlan):
             raise ValueError("adamw_plan: the lists differ in length")
         super().__init__(ctx, grads, (params, ms, vs, mss, vss, copies))
         self.state_bits = 8 if s8 else 32
-        arr = (PlanTensor * max(1, n))()
-        for i in range(n):
-            p, g, m, v, a = params[i], grads[i], ms[i], vs[i], arr[i]
+        packed, device = [], self.device
+        mtype, vtype = ((torch.int8,), (torch.uint8,)) if s8 else ((torch.float32,), (torch.float32,))
+        for p, g, m, v, ms_, vs_, c in zip(params, grads, ms, vs, mss, vss, copies):
             k = p.numel()
-            _check(p, "adamw_plan params", self.device, None, _FLOATS)
-            _check(g, "adamw_plan grads", self.device, k, _FLOATS)
-            _check(m, "adamw_plan exp_avgs", self.device, k, (torch.int8 if s8 else torch.float32,))
-            _check(v, "adamw_plan exp_avg_sqs", self.device, k, (torch.uint8 if s8 else torch.float32,))
-            a.numel, a.param_dtype, a.grad_dtype = k, _dtype_code(p), _dtype_code(g)
-            a.param, a.grad, a.exp_avg, a.exp_avg_sq = p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr()
+            _check(p, "adamw_plan params", device, None, _FLOATS)
+            _check(g, "adamw_plan grads", device, k, _FLOATS)
+            _check(m, "adamw_plan exp_avgs", device, k, mtype)
+            _check(v, "adamw_plan exp_avg_sqs", device, k, vtype)
             if s8:
-                for t in (mss[i], vss[i]):
-                    _check(t, "adamw_plan scales", self.device, state8_scales(k), (torch.float32,))
-                a.exp_avg_scale, a.exp_avg_sq_scale = mss[i].data_ptr(), vss[i].data_ptr()
-            if copies[i] is not None:
-                _check(copies[i], "adamw_plan param_copies", self.device, k, (torch.bfloat16,))
+                _check(ms_, "adamw_plan scales", device, state8_scales(k), (torch.float32,))
+                _check(vs_, "adamw_plan scales", device, state8_scales(k), (torch.float32,))
+            if c is not None:
+                _check(c, "adamw_plan param_copies", device, k, (torch.bfloat16,))
                 if p.dtype != torch.float32:
                     raise TypeError("adamw_plan: a bf16 copy goes with an fp32 parameter")
-                a.param_copy = copies[i].data_ptr()
+            packed.append(_PLAN_TENSOR.pack(k, _CODE[p.dtype], _CODE[g.dtype], p.data_ptr(), g.data_ptr(), m.data_ptr(),
+                                            v.data_ptr(), ms_.data_ptr() if s8 else 0, vs_.data_ptr() if s8 else 0,
+                                            0 if c is None else c.data_ptr()))
         self._default = default_adamw_plan_hparams()
         self._step = self._lib.muon_adamw_plan_step
-        self._create(self._lib.muon_adamw_plan_create, arr, n, self.state_bits)
+        self._create(self._lib.muon_adamw_plan_create, _array(PlanTensor, packed), n, self.state_bits)
 
     def step(self, step, hp: Optional[AdamwPlanHparams] = None, lr=None, grad_scale=None, seed: Optional[int] = None,
              stream=None):
@@ -214,11 +227,11 @@ class GradNormPlan(_GradPlan):
     def __init__(self, ctx, grads):
         grads = list(grads)
         super().__init__(ctx, grads, None)
-        arr = (GradTensor * max(1, len(grads)))()
-        for a, g in zip(arr, grads):
+        packed = []
+        for g in grads:
             _check(g, "grad_norm_plan", self.device, None, _FLOATS)
-            a.numel, a.grad_dtype, a.grad = g.numel(), _dtype_code(g), g.data_ptr()
-        self._create(self._lib.muon_grad_norm_plan_create, arr, len(grads))
+            packed.append(_GRAD_TENSOR.pack(g.numel(), _CODE[g.dtype], 0, g.data_ptr()))
+        self._create(self._lib.muon_grad_norm_plan_create, _array(GradTensor, packed), len(grads))
         n = ctypes.c_size_t()
         self._lib.muon_grad_norm_out_bytes(self._h, ctypes.byref(n))
         self._floats = n.value // 4
@@ -258,15 +271,15 @@ class State8Plan(_Plan):
         if len(codes) != n or len(scales) != n:
             raise ValueError("state8_plan: the lists differ in length")
         super().__init__(ctx, (values, codes, scales))
-        arr = (State8Tensor * max(1, n))()
-        for a, x, c, s in zip(arr, values, codes, scales):
+        packed = []
+        for x, c, s in zip(values, codes, scales):
             k = x.numel()
             _check(x, "state8_plan values", self.device, None, _FLOATS)
             _check(c, "state8_plan codes", self.device, k, (torch.int8, torch.uint8))
             _check(s, "state8_plan scales", self.device, state8_scales(k), (torch.float32,))
-            a.numel, a.value_dtype, a.second_moment = k, _dtype_code(x), int(c.dtype == torch.uint8)
-            a.values, a.codes, a.scales = x.data_ptr(), c.data_ptr(), s.data_ptr()
-        self._create(self._lib.muon_state8_plan_create, arr, n)
+            packed.append(_STATE8_TENSOR.pack(k, _CODE[x.dtype], c.dtype == torch.uint8, x.data_ptr(), c.data_ptr(),
+                                              s.data_ptr()))
+        self._create(self._lib.muon_state8_plan_create, _array(State8Tensor, packed), n)
 
     def pack(self, stream=None):
         """Values to codes and scales, rounded to nearest."""
