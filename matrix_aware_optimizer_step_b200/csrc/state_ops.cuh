@@ -2,12 +2,36 @@
 // the gradient norm that clips it, and the conversion of moments between the
 // two forms.  All are HBM-bound streams over lists of tensors.
 //
-//   adamw_plan_kernel  one AdamW step.  fp32 moments, or 8-bit codes with one
-//                      fp32 scale per 256 elements; fp32 or bf16 parameters,
-//                      fp32 parameters optionally with a bf16 working copy.
+//   adamw32_kernel     one AdamW step with fp32 moments; fp32 parameters,
+//                      optionally with a bf16 working copy, or bf16 ones.
+//   adamw8_kernel      the same step with 8-bit codes, one fp32 scale per 256
+//                      elements.
 //   grad_norm_kernel   norm = sqrt(sum g^2) over a list and the clip factor
 //                      min(1, max_norm / (norm + 1e-6)), one launch.
 //   state8_kernel      moments (fp32 or bf16) -> codes and scales, and back.
+//
+// Measured on 134M elements in one tensor, us and share of a plain copy's
+// 6.54 TB/s (a share above 1 is a better mix of reads and writes than the
+// copy's):
+//
+//   adamw32   fp32 parameters, bf16 gradients (26 B/element)     515   1.04
+//             ... with a copy (28)                               554   1.04
+//             bf16 parameters (22)                               437   1.03
+//             ... stochastic                                     467   0.97
+//   adamw8    fp32 parameters, bf16 gradients (14)               285   1.01
+//             ... with a copy (16)                               327   1.01
+//             ... stochastic                                     350   0.82
+//             bf16 parameters (10)                               249   0.83
+//             ... stochastic                                     377   0.55
+//   state8    pack from fp32 (10 for both moments)               210   0.98
+//             unpack to bf16 (6)                                 131   0.94
+//   norm      fp32 gradients (4)                                  83   0.99
+//             bf16 gradients (2), call after call                 42   0.97
+//
+// The 8-bit step on bf16 parameters and every stochastic one are bound by
+// instruction issue, not by memory (77 % of the issue slots used, the integer
+// pipe the busiest): two codes an element cost what two roots, their rounding
+// and its check cost, and a hash more when stochastic.
 //
 // The 8-bit form.  256 consecutive elements of one tensor are a block (one
 // warp, 8 elements per lane); codes keep the square root of the magnitude:
@@ -29,7 +53,7 @@
 // not finite as NaN throughout.
 //
 // Codes are defined by IEEE single-precision arithmetic in the order written
-// (adam_moments, encode_*): no contraction and no approximate function decides
+// (adam_moments8, encode_m, encode_r): no contraction and no approximate function decides
 // one, so the stored state does not depend on how a kernel is scheduled.
 #pragma once
 
@@ -526,9 +550,9 @@ __device__ __forceinline__ void block_bits(int64_t e, int lane, uint32_t key, ui
 }
 
 // New parameters to memory: bf16 (nearest or stochastic), or fp32 and its copy.
-template <bool PBF16, bool STOCH>
-__device__ __forceinline__ void store_param(char* param, __nv_bfloat16* copy, int lane, bool full, int count,
-                                            const float (&p)[8], const uint32_t (&h)[4]) {
+template <bool PBF16, bool COPY, bool STOCH>
+__device__ __forceinline__ void store_param(char* param, char* copy, int lane, bool full, int count, const float (&p)[8],
+                                            const uint32_t (&h)[4]) {
   uint32_t w[4];
   if (PBF16 && STOCH) {
     const bool odd = !(max_abs8(p) < INFINITY);     // a carry would turn a NaN's bits into a number
@@ -541,10 +565,10 @@ __device__ __forceinline__ void store_param(char* param, __nv_bfloat16* copy, in
         w[k] = __byte_perm(__float_as_uint(p[2 * k]) + (hp & 0xFFFFu), __float_as_uint(p[2 * k + 1]) + (hp >> 16), 0x7632);
     }
     store8_u16(param, lane, full, count, w);
-  } else if (PBF16 || copy != nullptr) {
+  } else if (PBF16 || COPY) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[k] = pack_bf16x2(p[2 * k], p[2 * k + 1]);
-    store8_u16(PBF16 ? param : reinterpret_cast<char*>(copy), lane, full, count, w);
+    store8_u16(PBF16 ? param : copy, lane, full, count, w);
   }
   if (!PBF16) store8_f32(param, lane, full, count, p);
 }
@@ -559,8 +583,10 @@ __device__ __forceinline__ void adam_param8(float (&p)[8], const float (&m)[8], 
   else adam_param8<false>(p, m, v, r, now.decay, now.step_size, now.inv_bc2, sc.eps2);
 }
 
-// fp32 moments: a block of 256 per warp, loaded straight to registers.
-template <bool PBF16, bool GBF16, bool STOCH>
+// fp32 moments: a block of 256 per warp, loaded straight to registers, ahead
+// of the launch's scalars.  Bound by HBM: 28 B an element leave the arithmetic
+// (29 instructions an element, start-up and all) a fifth of the issue slots.
+template <bool PBF16, bool COPY, bool GBF16, bool STOCH>
 __global__ void __launch_bounds__(ST_THREADS, 4)
     adamw32_kernel(const AdamChunk* __restrict__ chunks, const __grid_constant__ GradPtrs grads,
                    const __grid_constant__ AdamPlanScalars sc, const int* flags) {
@@ -574,7 +600,7 @@ __global__ void __launch_bounds__(ST_THREADS, 4)
   const char* grad = static_cast<const char*>(grads.p[ch.slot]) + (ch.base + first) * G;
   char *const pp = ch.param + first * P, *const mp = ch.m + first * 4, *const vp = ch.v + first * 4;
   const bool full = count >= Q_BLOCK && aligned(pp, 4 * P) && aligned(grad, 4 * G) && aligned(mp, 16) &&
-                    aligned(vp, 16) && aligned(ch.copy, 8);
+                    aligned(vp, 16) && (!COPY || aligned(ch.copy, 8));
   float g[8], p[8], m[8], v[8], r[8];
   pdl_wait();
   load8<GBF16>(grad, lane, full, count, g);
@@ -589,7 +615,7 @@ __global__ void __launch_bounds__(ST_THREADS, 4)
   store8_f32(vp, lane, full, count, v);
   uint32_t h[4] = {};
   if (STOCH) block_bits(ch.base + first, lane, mix32(mix32(sc.seed_key + now.step) + ch.id), h);
-  store_param<PBF16, STOCH>(pp, ch.copy == nullptr ? nullptr : ch.copy + first, lane, full, count, p, h);
+  store_param<PBF16, COPY, STOCH>(pp, reinterpret_cast<char*>(ch.copy + first), lane, full, count, p, h);
 }
 
 // 8-bit moments: up to Stage8::blocks blocks per warp, fetched whole into
@@ -597,7 +623,11 @@ __global__ void __launch_bounds__(ST_THREADS, 4)
 // block per warp left the start-up (about 210 instructions and two loads that
 // wait for one another) unpaid for: 134M elements, fp32 parameters, took 409
 // us with one block, 323 with two, 294 with three; as many as ADAM8_CTAS
-// resident thread blocks have shared memory for.
+// resident thread blocks have shared memory for.  Four thread blocks of 64
+// registers a thread beat three of 80 (304 and 310 us) and two (587 and 494 us
+// in an earlier form): the arithmetic needs the warps more than registers, so
+// what the loop over whole blocks keeps alive is kept small (the ragged tail
+// goes first, scales in one register, their pointers read again: 296 -> 285).
 template <bool PBF16, bool GBF16>
 struct Stage8 {
   static constexpr int P = PBF16 ? 2 : 4, G = GBF16 ? 2 : 4;
@@ -626,109 +656,142 @@ __device__ __forceinline__ bool bulk_wait(uint64_t* bar, int* flags) {
   return false;
 }
 
-template <bool PBF16, bool GBF16, bool STOCH>
+// A block's new moments to codes and scales, by the definition.
+template <bool STOCH>
+__device__ __forceinline__ void encode8_exact(const float (&m)[8], const float (&v)[8], float mscale, float rscale,
+                                              const uint32_t (&h)[4], uint32_t (&mw)[2], uint32_t (&vw)[2]) {
+  const float minv = scale_inverse(mscale), rinv = scale_inverse(rscale);
+  mw[0] = mw[1] = vw[0] = vw[1] = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float um = 0.5f, uv = 0.5f;
+    if (STOCH) {
+      const uint32_t hk = (h[k >> 1] >> (16 * (k & 1))) & 0xFFFFu;
+      uv = unit16(hk);
+      um = unit16(((hk >> 8) | (hk << 8)) & 0xFFFFu);
+    }
+    mw[k >> 2] |= encode_m(m[k], minv, um) << (8 * (k & 3));
+    vw[k >> 2] |= encode_r(__fsqrt_rn(v[k]), rinv, uv) << (8 * (k & 3));
+  }
+}
+
+// What a warp works on: its first element of each array.
+struct Adam8Warp {
+  char *param, *m, *v, *copy;
+  const char* grad;
+  int64_t base;
+  uint32_t key;
+};
+
+// Block b of a warp.  FULL: from shared memory, all 256 elements, vector
+// stores.  Else `count` elements from and to global memory one by one.
+// `scales`: lanes 2 b and 2 b + 1 hold the block's scales of m and of r, the
+// old ones on entry, the new ones on return.
+template <bool PBF16, bool COPY, bool GBF16, bool STOCH, bool FULL>
+__device__ __forceinline__ void adam8_block(const Adam8Warp& w, const char* mine, int b, int count, float& scales,
+                                            const AdamNow& now, const AdamPlanScalars& sc) {
+  using St = Stage8<PBF16, GBF16>;
+  const int lane = threadIdx.x & 31, at = b * Q_BLOCK;
+  float g[8], p[8], m[8], v[8], r[8];
+  uint32_t mw[2], vw[2];
+  load8<GBF16>((FULL ? mine + St::off_g : w.grad) + at * St::G, lane, FULL, count, g);
+  load8<PBF16>((FULL ? mine : w.param) + at * St::P, lane, FULL, count, p);
+  load8_codes((FULL ? mine + St::off_m : w.m) + at, lane, FULL, count, mw);
+  load8_codes((FULL ? mine + St::off_v : w.v) + at, lane, FULL, count, vw);
+  decode8_m(mw, __shfl_sync(0xffffffffu, scales, 2 * b), m);
+  decode8_v(vw, __shfl_sync(0xffffffffu, scales, 2 * b + 1), v);
+  adam_moments8(m, v, g, now.scale, sc);
+  adam_param8(p, m, v, r, now, sc);
+  uint32_t h[4] = {};
+  if (STOCH) block_bits(w.base + at, lane, w.key, h);
+  store_param<PBF16, COPY, STOCH>(w.param + at * St::P, COPY ? w.copy + at * 2 : nullptr, lane, FULL, count, p, h);
+  if (!FULL) {
+    // past the end m is 0 (no code, no gradient), but a code 0 of v is not
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (!inside(lane, k, count)) v[k] = 0.f;
+  }
+  const uint32_t mbits = __reduce_max_sync(0xffffffffu, __float_as_uint(max_abs8(m)));
+  const uint32_t vbits = __reduce_max_sync(0xffffffffu, __float_as_uint(max_abs8(v)));
+  // even lanes form the scale of m, odd ones that of r.  (Roots keep order:
+  // the largest root is the root of the largest.)
+  const bool second = lane & 1;
+  const float scale = block_scale(second ? __float_as_uint(__fsqrt_rn(__uint_as_float(vbits))) : mbits,
+                                  second ? 1.f / 65536.f : 1.f / 16129.f);
+  if (lane >> 1 == b) scales = scale;
+  const float mscale = __shfl_sync(0xffffffffu, scale, 0), rscale = __shfl_sync(0xffffffffu, scale, 1);
+  if (FULL && fast_block(mbits, vbits)) {
+    encode8_fast<false, STOCH>(m, m, mscale, h, mw);
+    encode8_fast<true, STOCH>(v, r, rscale, h, vw);
+  } else {
+    encode8_exact<STOCH>(m, v, mscale, rscale, h, mw, vw);
+  }
+  store8_codes(w.m + at, lane, FULL, count, mw);
+  store8_codes(w.v + at, lane, FULL, count, vw);
+}
+
+template <bool PBF16, bool COPY, bool GBF16, bool STOCH>
 __global__ void __launch_bounds__(ST_THREADS, ADAM8_CTAS)
     adamw8_kernel(const AdamChunk* __restrict__ chunks, int blocks, const __grid_constant__ GradPtrs grads,
                   const __grid_constant__ AdamPlanScalars sc, int* flags) {
   using St = Stage8<PBF16, GBF16>;
   extern __shared__ __align__(128) char smem[];
   __shared__ __align__(8) uint64_t bars[ST_WARPS];
-  const AdamChunk ch = chunks[blockIdx.x];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = warp * blocks * Q_BLOCK;
-  int count = min(static_cast<int>(ch.count) - first, blocks * Q_BLOCK);
-  if (count <= 0) return;
-  const char* grad = static_cast<const char*>(grads.p[ch.slot]) + (ch.base + first) * St::G;
-  char *pp = ch.param + first * St::P, *mp = ch.m + first, *vp = ch.v + first;
-  float *ms = ch.m_scale + first / Q_BLOCK, *vs = ch.v_scale + first / Q_BLOCK;
-  __nv_bfloat16* cp = ch.copy == nullptr ? nullptr : ch.copy + first;
-  // bulk copies want 16-byte boundaries; whole blocks have them when their
-  // tensors do.  What is left (a tensor's last block, views at odd offsets) is
-  // loaded where it is used.
-  const bool vec = aligned(pp, 16) && aligned(grad, 16) && aligned(mp, 16) && aligned(vp, 16) && aligned(cp, 8);
-  const int whole = vec ? count / Q_BLOCK : 0;
   const char* mine = smem + warp * St::bytes;
-  const uint32_t dst = smem_u32(mine), bar = smem_u32(&bars[warp]);
-  if (lane == 0) {
-    mbar_init(&bars[warp], 1);
-    fence_barrier_init();
-  }
-  __syncwarp();
-  pdl_wait();
-  if (whole > 0 && lane == 0) {
-    const uint32_t n = whole * Q_BLOCK;
-    mbar_arrive_expect_tx(&bars[warp], n * (St::P + St::G + 2));
-    bulk_load(dst + St::off_g, grad, n * St::G, bar);
-    bulk_load(dst, pp, n * St::P, bar);
-    bulk_load(dst + St::off_m, mp, n, bar);
-    bulk_load(dst + St::off_v, vp, n, bar);
-  }
-  // the scales of all the warp's blocks, one per lane
+  Adam8Warp w;
+  AdamNow now;
+  int whole, count;
   float scales = 0.f;
-  if ((lane >> 1) * Q_BLOCK < count) scales = (lane & 1 ? vs : ms)[lane >> 1];
-  const AdamNow now = adam_now(sc, flags);
+  {
+    // The table was complete before the first launch: it is read ahead of the
+    // wait for the previous kernel.
+    const AdamChunk ch = chunks[blockIdx.x];
+    count = min(static_cast<int>(ch.count) - first, blocks * Q_BLOCK);
+    if (count <= 0) return;
+    w.grad = static_cast<const char*>(grads.p[ch.slot]) + (ch.base + first) * St::G;
+    w.param = ch.param + first * St::P;
+    w.m = ch.m + first;
+    w.v = ch.v + first;
+    w.copy = COPY ? reinterpret_cast<char*>(ch.copy + first) : nullptr;
+    w.base = ch.base + first;
+    // bulk copies want 16-byte boundaries; whole blocks have them when their
+    // tensors do.  What is left (a tensor's last block, views at odd offsets)
+    // is loaded where it is used.
+    const bool vec = aligned(w.param, 16) && aligned(w.grad, 16) && aligned(w.m, 16) && aligned(w.v, 16) &&
+                     (!COPY || aligned(ch.copy, 8));
+    whole = vec ? count / Q_BLOCK : 0;
+    if (lane == 0) {
+      mbar_init(&bars[warp], 1);
+      fence_barrier_init();
+    }
+    __syncwarp();
+    pdl_wait();
+    if (whole > 0 && lane == 0) {
+      const uint32_t n = whole * Q_BLOCK, dst = smem_u32(mine), bar = smem_u32(&bars[warp]);
+      mbar_arrive_expect_tx(&bars[warp], n * (St::P + St::G + 2));
+      bulk_load(dst + St::off_g, w.grad, n * St::G, bar);
+      bulk_load(dst, w.param, n * St::P, bar);
+      bulk_load(dst + St::off_m, w.m, n, bar);
+      bulk_load(dst + St::off_v, w.v, n, bar);
+    }
+    if ((lane >> 1) * Q_BLOCK < count) scales = ((lane & 1 ? ch.v_scale : ch.m_scale) + first / Q_BLOCK)[lane >> 1];
+    now = adam_now(sc, flags);
+    w.key = STOCH ? mix32(mix32(sc.seed_key + now.step) + ch.id) : 0u;
+  }
+  if (now.go) {
+#pragma unroll 1
+    for (int b = whole; b * Q_BLOCK < count; ++b)
+      adam8_block<PBF16, COPY, GBF16, STOCH, false>(w, mine, b, count - b * Q_BLOCK, scales, now, sc);
+  }
   if (whole > 0 && !bulk_wait(&bars[warp], flags)) return;
   if (!now.go) return;
-  const uint32_t key = STOCH ? mix32(mix32(sc.seed_key + now.step) + ch.id) : 0u;
 #pragma unroll 1
-  for (int b = 0; count > 0; ++b, count -= Q_BLOCK) {
-    const bool full = b < whole;
-    const int at = b * Q_BLOCK;
-    float g[8], p[8], m[8], v[8], r[8];
-    uint32_t mw[2], vw[2];
-    if (full) {
-      load8<GBF16>(mine + St::off_g + at * St::G, lane, true, Q_BLOCK, g);
-      load8<PBF16>(mine + at * St::P, lane, true, Q_BLOCK, p);
-      load8_codes(mine + St::off_m + at, lane, true, Q_BLOCK, mw);
-      load8_codes(mine + St::off_v + at, lane, true, Q_BLOCK, vw);
-    } else {
-      load8<GBF16>(grad + at * St::G, lane, false, count, g);
-      load8<PBF16>(pp + at * St::P, lane, false, count, p);
-      load8_codes(mp + at, lane, false, count, mw);
-      load8_codes(vp + at, lane, false, count, vw);
-    }
-    decode8_m(mw, __shfl_sync(0xffffffffu, scales, 2 * b), m);
-    decode8_v(vw, __shfl_sync(0xffffffffu, scales, 2 * b + 1), v);
-    adam_moments8(m, v, g, now.scale, sc);
-    adam_param8(p, m, v, r, now, sc);
-    uint32_t h[4] = {};
-    if (STOCH) block_bits(ch.base + first + at, lane, key, h);
-    store_param<PBF16, STOCH>(pp + at * St::P, cp == nullptr ? nullptr : cp + at, lane, full, count, p, h);
-    // past the end m is 0 (no code, no gradient), but a code 0 of v is not
-    if (count < Q_BLOCK) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (!inside(lane, k, count)) v[k] = r[k] = 0.f;
-    }
-    const uint32_t mbits = __reduce_max_sync(0xffffffffu, __float_as_uint(max_abs8(m)));
-    const uint32_t vbits = __reduce_max_sync(0xffffffffu, __float_as_uint(max_abs8(v)));
-    // even lanes form the scale of m, odd ones that of r.  (Roots keep order:
-    // the largest root is the root of the largest.)
-    const bool second = lane & 1;
-    const float mine_scale = block_scale(second ? __float_as_uint(__fsqrt_rn(__uint_as_float(vbits))) : mbits,
-                                         second ? 1.f / 65536.f : 1.f / 16129.f);
-    if (lane < 2) (second ? vs : ms)[b] = mine_scale;
-    const float mscale = __shfl_sync(0xffffffffu, mine_scale, 0), rscale = __shfl_sync(0xffffffffu, mine_scale, 1);
-    if (fast_block(mbits, vbits)) {
-      encode8_fast<false, STOCH>(m, m, mscale, h, mw);
-      encode8_fast<true, STOCH>(v, r, rscale, h, vw);
-    } else {
-      const float minv = scale_inverse(mscale), rinv = scale_inverse(rscale);
-      mw[0] = mw[1] = vw[0] = vw[1] = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        float um = 0.5f, uv = 0.5f;
-        if (STOCH) {
-          const uint32_t hk = (h[k >> 1] >> (16 * (k & 1))) & 0xFFFFu;
-          uv = unit16(hk);
-          um = unit16(((hk >> 8) | (hk << 8)) & 0xFFFFu);
-        }
-        mw[k >> 2] |= encode_m(m[k], minv, um) << (8 * (k & 3));
-        vw[k >> 2] |= encode_r(__fsqrt_rn(v[k]), rinv, uv) << (8 * (k & 3));
-      }
-    }
-    store8_codes(mp + at, lane, full, count, mw);
-    store8_codes(vp + at, lane, full, count, vw);
-  }
+  for (int b = 0; b < whole; ++b) adam8_block<PBF16, COPY, GBF16, STOCH, true>(w, mine, b, Q_BLOCK, scales, now, sc);
+  // read again: kept, these pointers would cost the loop registers
+  const AdamChunk* ch = chunks + blockIdx.x;
+  if ((lane >> 1) * Q_BLOCK < min(static_cast<int>(ch->count) - first, blocks * Q_BLOCK))
+    ((lane & 1 ? ch->v_scale : ch->m_scale) + first / Q_BLOCK)[lane >> 1] = scales;
 }
 
 // ---------------------------------------------------------------------------

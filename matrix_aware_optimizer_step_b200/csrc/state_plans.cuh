@@ -18,7 +18,7 @@ enum PlanKind { PLAN_ADAMW, PLAN_NORM, PLAN_STATE8 };
 
 // One launch: up to MAX_SLOTS tensors of one combination of types.
 struct PlanBucket {
-  int pbf16 = 0, gbf16 = 0;
+  int pbf16 = 0, gbf16 = 0, copy = 0;
   std::vector<int> tensors;      // places in the plan's list; index = slot
   size_t first = 0, chunks = 0;  // in the plan's table
   int blocks = 1;                // of 256 elements, per warp (AdamW)
@@ -148,10 +148,10 @@ void fill_grads(const muon_plan* plan, const PlanBucket& b, GradPtrs& g) {
 }
 
 // Tensors of one key in list order, MAX_SLOTS per bucket.
-PlanBucket& bucket_for(muon_plan* plan, int pbf16, int gbf16) {
+PlanBucket& bucket_for(muon_plan* plan, int pbf16, int gbf16, int copy) {
   for (size_t k = plan->buckets.size(); k-- > 0;) {
     PlanBucket& b = plan->buckets[k];
-    if (b.pbf16 == pbf16 && b.gbf16 == gbf16) {
+    if (b.pbf16 == pbf16 && b.gbf16 == gbf16 && b.copy == copy) {
       if (b.tensors.size() < size_t(MAX_SLOTS)) return b;
       break;
     }
@@ -159,10 +159,11 @@ PlanBucket& bucket_for(muon_plan* plan, int pbf16, int gbf16) {
   plan->buckets.emplace_back();
   plan->buckets.back().pbf16 = pbf16;
   plan->buckets.back().gbf16 = gbf16;
+  plan->buckets.back().copy = copy;
   return plan->buckets.back();
 }
 
-template <bool S8, bool P, bool G, bool ST>
+template <bool S8, bool P, bool C, bool G, bool ST>
 cudaError_t launch_adamw(const muon_plan* plan, const PlanBucket& b, const GradPtrs& g, const AdamPlanScalars& sc,
                          int* flags, cudaStream_t st) {
   const AdamChunk* t = static_cast<const AdamChunk*>(plan->table) + b.first;
@@ -172,13 +173,13 @@ cudaError_t launch_adamw(const muon_plan* plan, const PlanBucket& b, const GradP
     static bool done[64] = {};
     const int dev = plan->device & 63;
     if (!done[dev]) {
-      const cudaError_t e = cudaFuncSetAttribute(adamw8_kernel<P, G, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      const cudaError_t e = cudaFuncSetAttribute(adamw8_kernel<P, C, G, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return e;
       done[dev] = true;
     }
-    return launch_pdl(adamw8_kernel<P, G, ST>, grid, dim3(ST_THREADS), size_t(smem), st, t, b.blocks, g, sc, flags);
+    return launch_pdl(adamw8_kernel<P, C, G, ST>, grid, dim3(ST_THREADS), size_t(smem), st, t, b.blocks, g, sc, flags);
   } else {
-    return launch_pdl(adamw32_kernel<P, G, ST>, grid, dim3(ST_THREADS), size_t(0), st, t, g, sc,
+    return launch_pdl(adamw32_kernel<P, C, G, ST>, grid, dim3(ST_THREADS), size_t(0), st, t, g, sc,
                       static_cast<const int*>(flags));
   }
 }
@@ -186,19 +187,20 @@ cudaError_t launch_adamw(const muon_plan* plan, const PlanBucket& b, const GradP
 using AdamLaunch = cudaError_t (*)(const muon_plan*, const PlanBucket&, const GradPtrs&, const AdamPlanScalars&, int*,
                                    cudaStream_t);
 
-// Stochastic rounding concerns codes and bf16 parameters: fp32 moments on fp32
-// parameters have nothing to round.
-AdamLaunch adamw_launcher(bool s8, bool p, bool g, bool stoch) {
-  if (s8) {
-    if (stoch)
-      return p ? (g ? launch_adamw<true, true, true, true> : launch_adamw<true, true, false, true>)
-               : (g ? launch_adamw<true, false, true, true> : launch_adamw<true, false, false, true>);
-    return p ? (g ? launch_adamw<true, true, true, false> : launch_adamw<true, true, false, false>)
-             : (g ? launch_adamw<true, false, true, false> : launch_adamw<true, false, false, false>);
-  }
-  if (stoch && p) return g ? launch_adamw<false, true, true, true> : launch_adamw<false, true, false, true>;
-  return p ? (g ? launch_adamw<false, true, true, false> : launch_adamw<false, true, false, false>)
-           : (g ? launch_adamw<false, false, true, false> : launch_adamw<false, false, false, false>);
+// A copy goes with fp32 parameters only.  Stochastic rounding concerns codes
+// and bf16 parameters: fp32 moments on fp32 parameters have nothing to round.
+template <bool S8, bool P, bool C>
+AdamLaunch pick_adamw(bool g, bool stoch) {
+  if (stoch && (S8 || P)) return g ? launch_adamw<S8, P, C, true, S8 || P> : launch_adamw<S8, P, C, false, S8 || P>;
+  return g ? launch_adamw<S8, P, C, true, false> : launch_adamw<S8, P, C, false, false>;
+}
+
+AdamLaunch adamw_launcher(bool s8, const PlanBucket& b, bool stoch) {
+  if (s8)
+    return b.pbf16 ? pick_adamw<true, true, false>(b.gbf16, stoch)
+                   : b.copy ? pick_adamw<true, false, true>(b.gbf16, stoch) : pick_adamw<true, false, false>(b.gbf16, stoch);
+  return b.pbf16 ? pick_adamw<false, true, false>(b.gbf16, stoch)
+                 : b.copy ? pick_adamw<false, false, true>(b.gbf16, stoch) : pick_adamw<false, false, false>(b.gbf16, stoch);
 }
 
 }  // namespace
@@ -253,7 +255,7 @@ muon_status muon_adamw_plan_create(muon_ctx* ctx, const muon_plan_tensor* tensor
       add_span(spans, t.exp_avg_scale, blocks * 4, true);
       add_span(spans, t.exp_avg_sq_scale, blocks * 4, true);
       add_span(spans, t.grad, t.numel * dtype_size(t.grad_dtype), false);
-      bucket_for(plan, t.param_dtype == MUON_BF16, t.grad_dtype == MUON_BF16).tensors.push_back(i);
+      bucket_for(plan, t.param_dtype == MUON_BF16, t.grad_dtype == MUON_BF16, t.param_copy != nullptr).tensors.push_back(i);
     }
     if (overlapping(spans))
       return fail(ctx, MUON_ERR_INVALID_ARG, "a tensor that the step writes overlaps another tensor of the plan");
@@ -349,7 +351,7 @@ muon_status muon_adamw_plan_step(muon_plan* plan, const muon_adamw_plan_hparams*
   ProfScope ps(ctx, MUON_K_ADAMW, st);
   for (const PlanBucket& b : plan->buckets) {
     fill_grads(plan, b, g);
-    const AdamLaunch f = adamw_launcher(plan->state_bits == 8, b.pbf16, b.gbf16, stochastic != 0);
+    const AdamLaunch f = adamw_launcher(plan->state_bits == 8, b, stochastic != 0);
     CUDA_TRY(ctx, f(plan, b, g, sc, ctx->dflags, st));
     ctx->launches++;
   }
@@ -372,7 +374,7 @@ muon_status muon_grad_norm_plan_create(muon_ctx* ctx, const muon_grad_tensor* te
       if (!t.grad) return fail(ctx, MUON_ERR_INVALID_ARG, "tensor %d: NULL pointer", i);
       if (!aligned_to(t.grad, dtype_size(t.grad_dtype)))
         return fail(ctx, MUON_ERR_INVALID_ARG, "tensor %d: a pointer is not aligned to its element", i);
-      bucket_for(plan, 0, 0).tensors.push_back(i);
+      bucket_for(plan, 0, 0, 0).tensors.push_back(i);
     }
     std::vector<NormChunk> table;
     const size_t most = size_t(device_sms(ctx->device)) * NORM_CTAS;
