@@ -546,7 +546,10 @@ __device__ __forceinline__ void block_bits(int64_t e, int lane, uint32_t key, ui
   const uint64_t q = static_cast<uint64_t>(e) / 2;
   const uint32_t low = static_cast<uint32_t>(q) ^ key ^ (2 * lane), high = static_cast<uint32_t>(q >> 32) * 0x9E3779B9u;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) h[k] = mix32((low ^ ((k >> 1) * (HALF / 2) + (k & 1))) + high);
+  for (int k = 0; k < 4; ++k) {
+    h[k] = mix32((low ^ ((k >> 1) * (HALF / 2) + (k & 1))) + high);
+    asm volatile("" : "+r"(h[k]));
+  }
 }
 
 // New parameters to memory: bf16 (nearest or stochastic), or fp32 and its copy.
