@@ -20,18 +20,18 @@
 //             ... stochastic                                     467   0.97
 //   adamw8    fp32 parameters, bf16 gradients (14)               285   1.01
 //             ... with a copy (16)                               327   1.01
-//             ... stochastic                                     350   0.82
-//             bf16 parameters (10)                               249   0.83
-//             ... stochastic                                     377   0.55
+//             ... stochastic                                     314   0.92
+//             bf16 parameters (10)                               250   0.83
+//             ... stochastic                                     350   0.59
 //   state8    pack from fp32 (10 for both moments)               210   0.98
 //             unpack to bf16 (6)                                 131   0.94
 //   norm      fp32 gradients (4)                                  83   0.99
 //             bf16 gradients (2), call after call                 42   0.97
 //
-// The 8-bit step on bf16 parameters and every stochastic one are bound by
-// instruction issue, not by memory (77 % of the issue slots used, the integer
-// pipe the busiest): two codes an element cost what two roots, their rounding
-// and its check cost, and a hash more when stochastic.
+// The 8-bit step on bf16 parameters and the stochastic ones are bound by
+// instruction issue, not by memory (56 and 67 instructions an element, 77 % of
+// the issue slots used, the integer pipe the busiest): two codes an element
+// cost two roots, their rounding and its check, and a hash when stochastic.
 //
 // The 8-bit form.  256 consecutive elements of one tensor are a block (one
 // warp, 8 elements per lane); codes keep the square root of the magnitude:
@@ -547,6 +547,8 @@ __device__ __forceinline__ void block_bits(int64_t e, int lane, uint32_t key, ui
   const uint32_t low = static_cast<uint32_t>(q) ^ key ^ (2 * lane), high = static_cast<uint32_t>(q >> 32) * 0x9E3779B9u;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
+    // kept as it is: the compiler would rather form it again for each of its
+    // uses, 11 instructions an element more (134M elements: 350 and 314 us)
     h[k] = mix32((low ^ ((k >> 1) * (HALF / 2) + (k & 1))) + high);
     asm volatile("" : "+r"(h[k]));
   }
