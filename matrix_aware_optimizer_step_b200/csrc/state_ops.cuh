@@ -29,7 +29,7 @@
 //             bf16 gradients (2), call after call                 42   0.97
 //
 // The 8-bit step on bf16 parameters and the stochastic ones are bound by
-// instruction issue, not by memory (56 and 67 instructions an element, 77 % of
+// instruction issue, not by memory (54 to 74 instructions an element, 78 % of
 // the issue slots used, the integer pipe the busiest): two codes an element
 // cost two roots, their rounding and its check, and a hash when stochastic.
 //
@@ -590,7 +590,7 @@ __device__ __forceinline__ void adam_param8(float (&p)[8], const float (&m)[8], 
 
 // fp32 moments: a block of 256 per warp, loaded straight to registers, ahead
 // of the launch's scalars.  Bound by HBM: 28 B an element leave the arithmetic
-// (29 instructions an element, start-up and all) a fifth of the issue slots.
+// (27 instructions an element, start-up and all) a fifth of the issue slots.
 template <bool PBF16, bool COPY, bool GBF16, bool STOCH>
 __global__ void __launch_bounds__(ST_THREADS, 4)
     adamw32_kernel(const AdamChunk* __restrict__ chunks, const __grid_constant__ GradPtrs grads,
