@@ -163,29 +163,34 @@ PlanBucket& bucket_for(muon_plan* plan, int pbf16, int gbf16, int copy) {
   return plan->buckets.back();
 }
 
+// Load a kernel on the current device ahead of its first launch, which may
+// happen inside a stream capture, where nothing should be loaded.
+template <typename... KArgs>
+cudaError_t load_kernel(void (*kernel)(KArgs...)) {
+  cudaFuncAttributes a;
+  return cudaFuncGetAttributes(&a, kernel);
+}
+
+// load: make the kernel ready instead of launching it.
 template <bool S8, bool P, bool C, bool G, bool ST>
 cudaError_t launch_adamw(const muon_plan* plan, const PlanBucket& b, const GradPtrs& g, const AdamPlanScalars& sc,
-                         int* flags, cudaStream_t st) {
+                         int* flags, cudaStream_t st, bool load) {
   const AdamChunk* t = static_cast<const AdamChunk*>(plan->table) + b.first;
   const dim3 grid{unsigned(b.chunks)};
   if constexpr (S8) {
     constexpr int smem = Stage8<P, G>::cta;
-    static bool done[64] = {};
-    const int dev = plan->device & 63;
-    if (!done[dev]) {
-      const cudaError_t e = cudaFuncSetAttribute(adamw8_kernel<P, C, G, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (e != cudaSuccess) return e;
-      done[dev] = true;
-    }
+    if (load)
+      return cudaFuncSetAttribute(adamw8_kernel<P, C, G, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     return launch_pdl(adamw8_kernel<P, C, G, ST>, grid, dim3(ST_THREADS), size_t(smem), st, t, b.blocks, g, sc, flags);
   } else {
+    if (load) return load_kernel(adamw32_kernel<P, C, G, ST>);
     return launch_pdl(adamw32_kernel<P, C, G, ST>, grid, dim3(ST_THREADS), size_t(0), st, t, g, sc,
                       static_cast<const int*>(flags));
   }
 }
 
 using AdamLaunch = cudaError_t (*)(const muon_plan*, const PlanBucket&, const GradPtrs&, const AdamPlanScalars&, int*,
-                                   cudaStream_t);
+                                   cudaStream_t, bool);
 
 // A copy goes with fp32 parameters only.  Stochastic rounding concerns codes
 // and bf16 parameters: fp32 moments on fp32 parameters have nothing to round.
@@ -295,6 +300,8 @@ muon_status muon_adamw_plan_create(muon_ctx* ctx, const muon_plan_tensor* tensor
         }
       }
       b.chunks = table.size() - b.first;
+      for (int stochastic = 0; stochastic < 2; ++stochastic)
+        CUDA_TRY(ctx, adamw_launcher(s8, b, stochastic != 0)(plan, b, GradPtrs{}, AdamPlanScalars{}, nullptr, nullptr, true));
     }
     return finish_plan(ctx, plan, table, out);
   });
@@ -352,7 +359,7 @@ muon_status muon_adamw_plan_step(muon_plan* plan, const muon_adamw_plan_hparams*
   for (const PlanBucket& b : plan->buckets) {
     fill_grads(plan, b, g);
     const AdamLaunch f = adamw_launcher(plan->state_bits == 8, b, stochastic != 0);
-    CUDA_TRY(ctx, f(plan, b, g, sc, ctx->dflags, st));
+    CUDA_TRY(ctx, f(plan, b, g, sc, ctx->dflags, st, false));
     ctx->launches++;
   }
   return MUON_OK;
@@ -390,6 +397,7 @@ muon_status muon_grad_norm_plan_create(muon_ctx* ctx, const muon_grad_tensor* te
       plan->norm_grid.push_back(unsigned(std::min(b.chunks, most)));
       plan->norm_ctas += plan->norm_grid.back();
     }
+    CUDA_TRY(ctx, load_kernel(grad_norm_kernel));
     return finish_plan(ctx, plan, table, out);
   });
 }
@@ -504,6 +512,8 @@ muon_status muon_state8_plan_create(muon_ctx* ctx, const muon_state8_tensor* ten
       return fail(ctx, MUON_ERR_INVALID_ARG, "two tensors of the plan overlap");
     plan->buckets.emplace_back();
     plan->buckets[0].chunks = table.size();
+    CUDA_TRY(ctx, load_kernel(state8_kernel<true>));
+    CUDA_TRY(ctx, load_kernel(state8_kernel<false>));
     return finish_plan(ctx, plan, table, out);
   });
 }

@@ -222,7 +222,9 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
         own = chain.from_iterable(g["params"] for g in self.param_groups)
         for k, p in zip(saved, own):
             for name, t in state_dict["state"].get(k, {}).items():
-                if isinstance(t, torch.Tensor):
+                if name == "step":
+                    self.state[p][name] = int(t)
+                elif isinstance(t, torch.Tensor):
                     dtype = torch.float32 if t.is_floating_point() else t.dtype
                     self.state[p][name] = t.detach().to(device=p.device, dtype=dtype, copy=True).contiguous()
         self._plans.clear()

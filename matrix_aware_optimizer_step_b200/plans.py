@@ -255,7 +255,7 @@ class GradNormPlan(_GradPlan):
         else:
             _check(out, "out", self.device, self._floats, (torch.float32,))
             result, ptr = out[:2], out.data_ptr()
-        st = self._run(self._h, max_norm, ptr, _current_stream(self.device) if stream is None else self._stream(stream))
+        st = self._run(self._h, float(max_norm), ptr, _current_stream(self.device) if stream is None else self._stream(stream))
         if st != MUON_OK:
             self._failed(st, "muon_grad_norm_run")
         return result

@@ -855,3 +855,35 @@ def test_one_tensor_past_2_to_33_elements_hashes_its_high_word(ctx, mx):
     assert np.array_equal(ms[first // 256:].cpu().numpy(), s) and np.array_equal(vs[first // 256:].cpu().numpy(), q)
     del p, g, m, v
     torch.cuda.empty_cache()
+
+
+@gpu
+def test_first_calls_of_a_process_inside_a_capture():
+    """Nothing is left to load or set up when a plan's first call is captured
+    (a new process: this one has loaded the kernels)."""
+    import subprocess
+    import sys
+    code = """
+import torch
+from matrix_aware_optimizer_step_b200 import MuonContext
+from matrix_aware_optimizer_step_b200.plans import state8_zeros
+ctx = MuonContext(0)
+p = torch.zeros(5000, device="cuda"); g = torch.ones(5000, device="cuda"); z = state8_zeros(p)
+out = torch.zeros(5000, device="cuda")
+m, v = torch.zeros(5000, device="cuda"), torch.zeros(5000, device="cuda")
+q = torch.zeros(5000, device="cuda", dtype=torch.bfloat16)
+a = ctx.adamw_plan([p], [g], [z["exp_avg"]], [z["exp_avg_sq"]], [z["exp_avg_scale"]], [z["exp_avg_sq_scale"]])
+b = ctx.adamw_plan([q], [g], [m], [v])
+n = ctx.grad_norm_plan([g]); u = ctx.state8_plan([out], [z["exp_avg"]], [z["exp_avg_scale"]])
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    f = n.run(10.0)
+    a.step(1, grad_scale=f[1:], seed=1); b.step(1, seed=2); u.unpack(); u.pack()
+graph.replay(); torch.cuda.synchronize()
+assert abs(float(f[0]) - 5000 ** 0.5) < 1e-3 and bool((p < 0).all()) and bool((q < 0).all()) and bool((out > 0).all())
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
