@@ -18,18 +18,19 @@
 //             ... with a copy (28)                               554   1.04
 //             bf16 parameters (22)                               437   1.03
 //             ... stochastic                                     467   0.97
-//   adamw8    fp32 parameters, bf16 gradients (14)               285   1.01
-//             ... with a copy (16)                               327   1.01
-//             ... stochastic                                     314   0.92
-//             bf16 parameters (10)                               250   0.83
-//             ... stochastic                                     350   0.59
-//   state8    pack from fp32 (10 for both moments)               210   0.98
+//   adamw8    fp32 parameters, bf16 gradients (14)               283   1.02
+//             ... with a copy (16)                               324   1.02
+//             ... with a copy, stochastic                        334   0.98
+//             ... stochastic                                     307   0.94
+//             bf16 parameters (10)                               244   0.85
+//             ... stochastic                                     324   0.64
+//   state8    pack from fp32 (10 for both moments)               206   1.00
 //             unpack to bf16 (6)                                 131   0.94
 //   norm      fp32 gradients (4)                                  83   0.99
 //             bf16 gradients (2), call after call                 42   0.97
 //
 // The 8-bit step on bf16 parameters and the stochastic ones are bound by
-// instruction issue, not by memory (54 to 74 instructions an element, 78 % of
+// instruction issue, not by memory (52 to 72 instructions an element, 78 % of
 // the issue slots used, the integer pipe the busiest): two codes an element
 // cost two roots, their rounding and its check, and a hash when stochastic.
 //
@@ -243,6 +244,14 @@ __device__ __forceinline__ float block_scale(uint32_t max_bits, float inv_levels
   return max_bits >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : max_bits < __float_as_uint(Q_TINY) ? 0.f : s;
 }
 
+// ... of first moments from the largest |m|, of second ones from the largest v
+// (roots keep order: the largest root is the root of the largest).
+template <bool SECOND>
+__device__ __forceinline__ float moment_scale(uint32_t max_bits) {
+  return SECOND ? block_scale(__float_as_uint(__fsqrt_rn(__uint_as_float(max_bits))), 1.f / 65536.f)
+                : block_scale(max_bits, 1.f / 16129.f);
+}
+
 // 1 / s, 0 for a block that keeps no codes.
 __device__ __forceinline__ float scale_inverse(float s) { return s > 0.f ? __frcp_rn(s) : 0.f; }
 
@@ -273,15 +282,16 @@ __device__ __forceinline__ uint32_t encode_r(float r, float inv, float u) {
 // definition.  A 16-bit u enters as h / 2^16 - 1/2, short of its 2^-17.
 //
 // Errors of y on both sides together, relative in units of 2^-23 (an IEEE
-// operation has 1/2, an approximate one 1), halved by the root where they
-// stand under it:
-//   m: 1 / s 1.5, times m 1 -> 1.25; the root 1.5; times 127: 4.2e-5.  y + u:
-//      2^-17 in the definition, 2^-18 twice here, 2^-17 for the missing part
-//      of u: 2.3e-5.
-//   r: r 1.5, 1 / s 1.5, the product 1 -> 2; the root 1.5; times 256: 1.07e-4.
-//      y + u: three times 2^-17 and 2^-18: 2.7e-5.
-constexpr float FAR_M = 0.5f - 6.8e-5f;
-constexpr float FAR_R = 0.5f - 1.4e-4f;
+// operation has 1/2, an approximate one 1, rsqrt.approx 1.1), halved by the
+// root where they stand under it:
+//   m: 1 / s 1 + 1/2 here and 1 in the definition, whose 1 / 127^2 is off by
+//      0.16, times m 1 -> 1.83; the root 1.5; times 127: 5.1e-5.  y + u: 2^-17 in the definition, 2^-18 twice
+//      here, 2^-17 for the missing part of u: 2.3e-5.
+//   r: r 1.5, 1 / s 1.1 here and 1 in the definition, the product 1 -> 2.3;
+//      the root 1.5; times 256: 1.16e-4.  y + u: three times 2^-17 and 2^-18:
+//      2.7e-5.
+constexpr float FAR_M = 0.5f - 7.5e-5f;
+constexpr float FAR_R = 0.5f - 1.46e-4f;
 constexpr float ROUND_MAGIC = 12582912.f;   // 1.5 * 2^23
 
 __device__ __forceinline__ float sqrt_fast(float x) {
@@ -294,6 +304,19 @@ __device__ __forceinline__ float rcp_fast(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float rsqrt_fast(float x) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 1 / s on the fast path, straight from the largest |m| or v.
+template <bool SECOND>
+__device__ __forceinline__ float fast_inverse(uint32_t max_bits) {
+  const float big = __uint_as_float(max_bits);
+  return SECOND ? 65536.f * rsqrt_fast(big) : 16129.f * rcp_fast(big);
 }
 
 // max(a, |b|, |c|), NaN if any is
@@ -393,9 +416,10 @@ __device__ __forceinline__ bool round8(const float (&x)[8], float inv, const uin
 // Forms the codes that round8 could not be sure of by their definition, one a
 // pass: almost always a single one of a warp's 256.
 template <bool SECOND, bool STOCH>
-__device__ __forceinline__ void redo8(const float (&x)[8], float s, const uint32_t (&h)[4], const float (&a)[8], float (&z)[8]) {
+__device__ __forceinline__ void redo8(const float (&x)[8], uint32_t max_bits, const uint32_t (&h)[4], const float (&a)[8],
+                                      float (&z)[8]) {
   constexpr float MAGIC = SECOND ? ROUND_MAGIC - 1.f : ROUND_MAGIC, FAR = SECOND ? FAR_R : FAR_M;
-  const float inv = __frcp_rn(s);
+  const float inv = __frcp_rn(moment_scale<SECOND>(max_bits));
   uint32_t todo = 0;
 #pragma unroll
   for (int k = 0; k < 8; ++k) todo |= (fabsf(a[k] - (z[k] - MAGIC)) > FAR ? 1u : 0u) << k;
@@ -421,12 +445,12 @@ __device__ __forceinline__ void redo8(const float (&x)[8], float s, const uint32
 }
 
 // Codes of 8 first moments (x = r = m) or second moments (x = v, r its fast
-// root) on the fast path.
+// root) on the fast path; max_bits: the largest |m| or v of the block.
 template <bool SECOND, bool STOCH>
-__device__ __forceinline__ void encode8_fast(const float (&x)[8], const float (&r)[8], float s, const uint32_t (&h)[4],
-                                             uint32_t (&w)[2]) {
+__device__ __forceinline__ void encode8_fast(const float (&x)[8], const float (&r)[8], uint32_t max_bits,
+                                             const uint32_t (&h)[4], uint32_t (&w)[2]) {
   float a[8], z[8];
-  if (round8<SECOND, STOCH>(r, rcp_fast(s), h, a, z)) redo8<SECOND, STOCH>(x, s, h, a, z);
+  if (round8<SECOND, STOCH>(r, fast_inverse<SECOND>(max_bits), h, a, z)) redo8<SECOND, STOCH>(x, max_bits, h, a, z);
   w[0] = pack_low_bytes(z, 0);
   w[1] = pack_low_bytes(z, 4);
 }
@@ -456,10 +480,10 @@ __device__ __forceinline__ void decode8_v(const uint32_t (&w)[2], float s, float
 // Blocks that the fast path takes: its flushes of subnormals then change no
 // code (an element whose v is subnormal lies below 2^-36 of the block's
 // largest, code 0 on either path).
-constexpr float FAST_V_MIN = 8.0779356694631609e-28f;   // 2^-90
 __device__ __forceinline__ bool fast_block(uint32_t mbits, uint32_t vbits) {
-  return mbits >= __float_as_uint(Q_TINY) && mbits < 0x7F800000u && vbits >= __float_as_uint(FAST_V_MIN) &&
-         vbits < 0x7F800000u;
+  constexpr uint32_t m_low = 0x0D800000u, m_top = 0x7B800000u;     // 2^-100, 2^120: 1 / m stays a normal number
+  constexpr uint32_t v_low = 0x12800000u, v_top = 0x7F800000u;     // 2^-90, infinity
+  return mbits - m_low < m_top - m_low && vbits - v_low < v_top - v_low;
 }
 
 // New moments, each operation rounded once.  A packed mul whose result goes
@@ -631,8 +655,12 @@ __global__ void __launch_bounds__(ST_THREADS, 4)
 // resident thread blocks have shared memory for.  Four thread blocks of 64
 // registers a thread beat three of 80 (304 and 310 us) and two (587 and 494 us
 // in an earlier form): the arithmetic needs the warps more than registers, so
-// what the loop over whole blocks keeps alive is kept small (the ragged tail
-// goes first, scales in one register, their pointers read again: 296 -> 285).
+// what the loop over whole blocks keeps alive is kept small: the ragged tail
+// goes first, scales stay in one register, their pointers are read again (296
+// -> 285); new scales are formed once for all of a warp's blocks, from their
+// largest magnitudes (285 -> 283, bf16 parameters 250 -> 244); the copy's
+// pointer is read again for each block (327 -> 324, stochastic 373 -> 334; m's
+// and v's as well cost more than they freed).
 template <bool PBF16, bool GBF16>
 struct Stage8 {
   static constexpr int P = PBF16 ? 2 : 4, G = GBF16 ? 2 : 4;
@@ -663,9 +691,9 @@ __device__ __forceinline__ bool bulk_wait(uint64_t* bar, int* flags) {
 
 // A block's new moments to codes and scales, by the definition.
 template <bool STOCH>
-__device__ __forceinline__ void encode8_exact(const float (&m)[8], const float (&v)[8], float mscale, float rscale,
+__device__ __forceinline__ void encode8_exact(const float (&m)[8], const float (&v)[8], uint32_t mbits, uint32_t vbits,
                                               const uint32_t (&h)[4], uint32_t (&mw)[2], uint32_t (&vw)[2]) {
-  const float minv = scale_inverse(mscale), rinv = scale_inverse(rscale);
+  const float minv = scale_inverse(moment_scale<false>(mbits)), rinv = scale_inverse(moment_scale<true>(vbits));
   mw[0] = mw[1] = vw[0] = vw[1] = 0;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
@@ -680,9 +708,10 @@ __device__ __forceinline__ void encode8_exact(const float (&m)[8], const float (
   }
 }
 
-// What a warp works on: its first element of each array.
+// What a warp works on: its first element in the chunk and of each array.
 struct Adam8Warp {
-  char *param, *m, *v, *copy;
+  char *param, *m, *v;
+  int first;
   const char* grad;
   int64_t base;
   uint32_t key;
@@ -690,11 +719,12 @@ struct Adam8Warp {
 
 // Block b of a warp.  FULL: from shared memory, all 256 elements, vector
 // stores.  Else `count` elements from and to global memory one by one.
-// `scales`: lanes 2 b and 2 b + 1 hold the block's scales of m and of r, the
-// old ones on entry, the new ones on return.
+// `scales`: lanes 2 b and 2 b + 1 hold the block's old scales of m and of r on
+// entry, its largest new |m| and v on return, from which the warp forms the
+// scales of all its blocks at once.
 template <bool PBF16, bool COPY, bool GBF16, bool STOCH, bool FULL>
 __device__ __forceinline__ void adam8_block(const Adam8Warp& w, const char* mine, int b, int count, float& scales,
-                                            const AdamNow& now, const AdamPlanScalars& sc) {
+                                            const AdamNow& now, const AdamPlanScalars& sc, const AdamChunk* ch) {
   using St = Stage8<PBF16, GBF16>;
   const int lane = threadIdx.x & 31, at = b * Q_BLOCK;
   float g[8], p[8], m[8], v[8], r[8];
@@ -709,7 +739,7 @@ __device__ __forceinline__ void adam8_block(const Adam8Warp& w, const char* mine
   adam_param8(p, m, v, r, now, sc);
   uint32_t h[4] = {};
   if (STOCH) block_bits(w.base + at, lane, w.key, h);
-  store_param<PBF16, COPY, STOCH>(w.param + at * St::P, COPY ? w.copy + at * 2 : nullptr, lane, FULL, count, p, h);
+  store_param<PBF16, COPY, STOCH>(w.param + at * St::P, COPY ? reinterpret_cast<char*>(ch->copy + w.first + at) : nullptr, lane, FULL, count, p, h);
   if (!FULL) {
     // past the end m is 0 (no code, no gradient), but a code 0 of v is not
 #pragma unroll
@@ -718,20 +748,14 @@ __device__ __forceinline__ void adam8_block(const Adam8Warp& w, const char* mine
   }
   const uint32_t mbits = __reduce_max_sync(0xffffffffu, __float_as_uint(max_abs8(m)));
   const uint32_t vbits = __reduce_max_sync(0xffffffffu, __float_as_uint(max_abs8(v)));
-  // even lanes form the scale of m, odd ones that of r.  (Roots keep order:
-  // the largest root is the root of the largest.)
-  const bool second = lane & 1;
-  const float scale = block_scale(second ? __float_as_uint(__fsqrt_rn(__uint_as_float(vbits))) : mbits,
-                                  second ? 1.f / 65536.f : 1.f / 16129.f);
-  if (lane >> 1 == b) scales = scale;
-  const float mscale = __shfl_sync(0xffffffffu, scale, 0), rscale = __shfl_sync(0xffffffffu, scale, 1);
+  if (lane >> 1 == b) scales = __uint_as_float(lane & 1 ? vbits : mbits);
   // (a stochastic tail on the fast path cost the loop over whole blocks
   // registers: 183 -> 188 us on 38.7M elements with the clip and unpacking)
   if ((FULL || !STOCH) && fast_block(mbits, vbits)) {
-    encode8_fast<false, STOCH>(m, m, mscale, h, mw);
-    encode8_fast<true, STOCH>(v, r, rscale, h, vw);
+    encode8_fast<false, STOCH>(m, m, mbits, h, mw);
+    encode8_fast<true, STOCH>(v, r, vbits, h, vw);
   } else {
-    encode8_exact<STOCH>(m, v, mscale, rscale, h, mw, vw);
+    encode8_exact<STOCH>(m, v, mbits, vbits, h, mw, vw);
   }
   store8_codes(w.m + at, lane, FULL, count, mw);
   store8_codes(w.v + at, lane, FULL, count, vw);
@@ -760,7 +784,7 @@ __global__ void __launch_bounds__(ST_THREADS, ADAM8_CTAS)
     w.param = ch.param + first * St::P;
     w.m = ch.m + first;
     w.v = ch.v + first;
-    w.copy = COPY ? reinterpret_cast<char*>(ch.copy + first) : nullptr;
+    w.first = first;
     w.base = ch.base + first;
     // bulk copies want 16-byte boundaries; whole blocks have them when their
     // tensors do.  What is left (a tensor's last block, views at odd offsets)
@@ -789,16 +813,18 @@ __global__ void __launch_bounds__(ST_THREADS, ADAM8_CTAS)
   if (now.go) {
 #pragma unroll 1
     for (int b = whole; b * Q_BLOCK < count; ++b)
-      adam8_block<PBF16, COPY, GBF16, STOCH, false>(w, mine, b, count - b * Q_BLOCK, scales, now, sc);
+      adam8_block<PBF16, COPY, GBF16, STOCH, false>(w, mine, b, count - b * Q_BLOCK, scales, now, sc, chunks + blockIdx.x);
   }
   if (whole > 0 && !bulk_wait(&bars[warp], flags)) return;
   if (!now.go) return;
 #pragma unroll 1
-  for (int b = 0; b < whole; ++b) adam8_block<PBF16, COPY, GBF16, STOCH, true>(w, mine, b, Q_BLOCK, scales, now, sc);
+  for (int b = 0; b < whole; ++b) adam8_block<PBF16, COPY, GBF16, STOCH, true>(w, mine, b, Q_BLOCK, scales, now, sc, chunks + blockIdx.x);
   // read again: kept, these pointers would cost the loop registers
   const AdamChunk* ch = chunks + blockIdx.x;
+  const uint32_t bits = __float_as_uint(scales);
+  const float ms = moment_scale<false>(bits), rs = moment_scale<true>(bits);
   if ((lane >> 1) * Q_BLOCK < min(static_cast<int>(ch->count) - first, blocks * Q_BLOCK))
-    ((lane & 1 ? ch->v_scale : ch->m_scale) + first / Q_BLOCK)[lane >> 1] = scales;
+    ((lane & 1 ? ch->v_scale : ch->m_scale) + first / Q_BLOCK)[lane >> 1] = lane & 1 ? rs : ms;
 }
 
 // ---------------------------------------------------------------------------
@@ -828,16 +854,16 @@ __device__ __forceinline__ void pack8(float (&x)[8], float* scale, int lane, uin
     for (int k = 0; k < 8; ++k) low = fminf(low, x[k]);
     plain = __all_sync(0xffffffffu, low == 0.f);
   }
-  const uint32_t bits = !plain ? 0x7FC00000u : SECOND ? __float_as_uint(__fsqrt_rn(__uint_as_float(xbits))) : xbits;
-  const float s = block_scale(bits, SECOND ? 1.f / 65536.f : 1.f / 16129.f);
+  const uint32_t bits = plain ? xbits : 0x7FC00000u;
+  const float s = moment_scale<SECOND>(bits);
   if (lane == 0) *scale = s;
   const uint32_t none[4] = {};
   w[0] = w[1] = 0;
-  if (plain && fast_block(SECOND ? __float_as_uint(1.f) : xbits, SECOND ? xbits : __float_as_uint(1.f))) {
+  if (fast_block(SECOND ? __float_as_uint(1.f) : bits, SECOND ? bits : __float_as_uint(1.f))) {
     float r[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) r[k] = SECOND ? sqrt_fast(x[k]) : x[k];
-    encode8_fast<SECOND, false>(x, r, s, none, w);
+    encode8_fast<SECOND, false>(x, r, bits, none, w);
   } else {
     const float inv = scale_inverse(s);
 #pragma unroll

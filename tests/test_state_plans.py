@@ -887,3 +887,20 @@ print("captured")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+@gpu
+@pytest.mark.parametrize("mag", [1e-33, 1e-29, 1e-20, 1e20, 1e36, 1e37, 3e38])
+def test_state8_conversion_over_the_range_of_fp32(ctx, mag):
+    """Blocks either side of what the fast path takes, up to fp32's largest
+    values: codes and scales bit for bit."""
+    rng = np.random.default_rng(40)
+    m = (rng.uniform(-1, 1, 2100) ** 3 * mag).astype(np.float32)
+    v = np.abs(m)
+    cm, cv = torch.zeros(2100, dtype=torch.int8, device="cuda"), torch.zeros(2100, dtype=torch.uint8, device="cuda")
+    sm, sv = torch.zeros(9, device="cuda"), torch.zeros(9, device="cuda")
+    ctx.state8_plan([torch.from_numpy(m).cuda(), torch.from_numpy(v).cuda()], [cm, cv], [sm, sv]).pack()
+    torch.cuda.synchronize()
+    (c, s), (d, q) = ref.encode_m(m), ref.encode_v(v)
+    assert np.array_equal(cm.cpu().numpy(), c) and np.array_equal(sm.cpu().numpy(), s)
+    assert np.array_equal(cv.cpu().numpy(), d) and np.array_equal(sv.cpu().numpy(), q)
