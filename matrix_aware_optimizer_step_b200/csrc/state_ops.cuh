@@ -20,7 +20,7 @@
 //             ... stochastic                                     467   0.97
 //   adamw8    fp32 parameters, bf16 gradients (14)               283   1.02
 //             ... with a copy (16)                               324   1.02
-//             ... with a copy, stochastic                        334   0.98
+//             ... with a copy, stochastic                        326   1.01
 //             ... stochastic                                     307   0.94
 //             bf16 parameters (10)                               244   0.85
 //             ... stochastic                                     324   0.64
@@ -658,9 +658,10 @@ __global__ void __launch_bounds__(ST_THREADS, 4)
 // what the loop over whole blocks keeps alive is kept small: the ragged tail
 // goes first, scales stay in one register, their pointers are read again (296
 // -> 285); new scales are formed once for all of a warp's blocks, from their
-// largest magnitudes (285 -> 283, bf16 parameters 250 -> 244); the copy's
-// pointer is read again for each block (327 -> 324, stochastic 373 -> 334; m's
-// and v's as well cost more than they freed).
+// largest magnitudes (285 -> 283, bf16 parameters 250 -> 244); with a copy,
+// its pointer and its place in the tensor are read again for each block (327
+// -> 324, stochastic 373 -> 326; the place without a copy, or m's and v's
+// pointers, cost more than they freed).
 template <bool PBF16, bool GBF16>
 struct Stage8 {
   static constexpr int P = PBF16 ? 2 : 4, G = GBF16 ? 2 : 4;
@@ -738,7 +739,7 @@ __device__ __forceinline__ void adam8_block(const Adam8Warp& w, const char* mine
   adam_moments8(m, v, g, now.scale, sc);
   adam_param8(p, m, v, r, now, sc);
   uint32_t h[4] = {};
-  if (STOCH) block_bits(w.base + at, lane, w.key, h);
+  if (STOCH) block_bits((COPY ? ch->base + w.first : w.base) + at, lane, w.key, h);
   store_param<PBF16, COPY, STOCH>(w.param + at * St::P, COPY ? reinterpret_cast<char*>(ch->copy + w.first + at) : nullptr, lane, FULL, count, p, h);
   if (!FULL) {
     // past the end m is 0 (no code, no gradient), but a code 0 of v is not
