@@ -90,6 +90,8 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        if any(g.get("state_bits", 32) not in (8, 32) for g in self.param_groups):
+            raise ValueError("state_bits must be 8 or 32")
         for i, g in enumerate(self.param_groups):
             params = [p for p in g["params"] if p.grad is not None]
             if not params:

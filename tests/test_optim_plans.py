@@ -228,3 +228,19 @@ def test_plans_do_not_keep_gradients_alive():
     opt.step()
     opt.zero_grad(set_to_none=True)
     assert torch.cuda.memory_allocated() == held
+
+
+@gpu
+def test_refuses_state_bits_changed_to_a_form_that_is_not_there():
+    from matrix_aware_optimizer_step_b200.optim import MuonWithAuxAdam
+    ps = params()
+    opt = MuonWithAuxAdam([dict(params=ps, use_muon=False)])
+    before = [p.detach().clone() for p in ps]
+    grad(ps, 1)
+    opt.param_groups[0]["state_bits"] = 16
+    with pytest.raises(ValueError):
+        opt.step()
+    assert all(torch.equal(p, q) for p, q in zip(ps, before))
+    opt.param_groups[0]["state_bits"] = 8
+    opt.step()
+    assert not torch.equal(ps[0], before[0])
