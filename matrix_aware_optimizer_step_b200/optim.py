@@ -32,6 +32,20 @@ ADAMW_DEFAULTS = dict(lr=3e-4, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.01, s
                       max_grad_norm=None, seed=None)
 
 
+def _own_types(state, p):
+    """A parameter's saved state on its device, copied: codes as they are,
+    other tensors in fp32, the step a number."""
+    out = {}
+    for name, t in state.items():
+        if name == "step":
+            t = int(t)
+        elif isinstance(t, torch.Tensor):
+            dtype = torch.float32 if t.is_floating_point() else t.dtype
+            t = t.detach().to(device=p.device, dtype=dtype, copy=True).contiguous()
+        out[name] = t
+    return out
+
+
 class MuonWithAuxAdam(torch.optim.Optimizer):
     """Muon for groups with use_muon=True (parameters of two or more
     dimensions, stepped as rows x prod(other dims) matrices), AdamW for the
@@ -218,15 +232,23 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
         """As torch.optim.Optimizer's, except that 8-bit codes stay what they
         are and every other state tensor becomes fp32 (the base class casts
         state to the parameter's type, which would round the moments and
-        scales of bf16 parameters and turn codes into numbers)."""
-        super().load_state_dict(state_dict)
-        saved = chain.from_iterable(g["params"] for g in state_dict["param_groups"])
-        own = chain.from_iterable(g["params"] for g in self.param_groups)
-        for k, p in zip(saved, own):
-            for name, t in state_dict["state"].get(k, {}).items():
-                if name == "step":
-                    self.state[p][name] = int(t)
-                elif isinstance(t, torch.Tensor):
-                    dtype = torch.float32 if t.is_floating_point() else t.dtype
-                    self.state[p][name] = t.detach().to(device=p.device, dtype=dtype, copy=True).contiguous()
-        self._plans.clear()
+        scales of bf16 parameters and turn codes into numbers).  Pre-hooks
+        come before this and post-hooks after it."""
+        fresh = {}
+
+        def last_pre_hook(opt, sd):
+            saved = chain.from_iterable(g["params"] for g in sd["param_groups"])
+            own = dict(zip(saved, chain.from_iterable(g["params"] for g in self.param_groups)))
+            fresh.update((own[k], _own_types(st, own[k])) for k, st in sd["state"].items() if k in own)
+
+        def first_post_hook(opt):
+            self.state.update(fresh)
+            self._plans.clear()
+
+        hooks = [self.register_load_state_dict_pre_hook(last_pre_hook),
+                 self.register_load_state_dict_post_hook(first_post_hook, prepend=True)]
+        try:
+            super().load_state_dict(state_dict)
+        finally:
+            for h in hooks:
+                h.remove()
