@@ -240,6 +240,8 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
             saved = chain.from_iterable(g["params"] for g in sd["param_groups"])
             own = dict(zip(saved, chain.from_iterable(g["params"] for g in self.param_groups)))
             fresh.update((own[k], _own_types(st, own[k])) for k, st in sd["state"].items() if k in own)
+            # no tensor is left for the base class, whose cast would hold every 8-bit moment in 32 bits at once
+            return dict(sd, state={k: st for k, st in sd["state"].items() if k not in own})
 
         def first_post_hook(opt):
             self.state.update(fresh)

@@ -117,6 +117,27 @@ def test_types_copies_and_state_of_no_parameter(make):
     assert two.state["elsewhere"] == {"kept": 1} and not two._plans
 
 
+def test_tensors_never_take_the_parameters_type(make, monkeypatch):
+    """No code passes through a floating type on its way in: the largest new
+    tensor of a load is as large as the saved one."""
+    a, = params(1)
+    one = make([a], state_bits=8)
+    eight_bit(one, a, 3)
+    c, = params(1)
+    two = make([c], state_bits=8)
+    made = []
+    to = torch.Tensor.to
+
+    def spy(self, *args, **kw):
+        r = to(self, *args, **kw)
+        made.append((self.dtype, r.dtype))
+        return r
+
+    monkeypatch.setattr(torch.Tensor, "to", spy)
+    two.load_state_dict(one.state_dict())
+    assert made and not [x for x in made if x[0] in (torch.int8, torch.uint8) and x[1] != x[0]]
+
+
 def test_a_load_that_fails_changes_nothing(make):
     a, b = params(2)
     one = make([a, b], state_bits=8)
