@@ -529,7 +529,8 @@ struct AdamNow {
   bool go;                 // false: nothing is written
 };
 
-// Every lane of a warp calls it.
+// Every lane of a warp calls it, and all get the same answer: blocks are
+// reduced over whole warps.
 __device__ __forceinline__ AdamNow adam_now(const AdamPlanScalars& sc, const int* flags) {
   AdamNow d{1.f, sc.step_size, sc.inv_bc2, sc.decay, sc.step, true};
   const bool stop = halted(flags);
@@ -558,7 +559,7 @@ __device__ __forceinline__ AdamNow adam_now(const AdamPlanScalars& sc, const int
     d.step_size = __shfl_sync(0xffffffffu, d.step_size, 0);
     d.inv_bc2 = __shfl_sync(0xffffffffu, d.inv_bc2, 0);
   }
-  d.go = d.go && !stop;
+  d.go = __all_sync(0xffffffffu, d.go && !stop);
   return d;
 }
 
@@ -678,8 +679,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 
 // Waits for the warp's bulk copies.  After kWaitLimitNs it records that in the
 // context's flags, gives copies in flight as long again to land before the
-// shared memory is given back, and returns false.
-__device__ __forceinline__ bool bulk_wait(uint64_t* bar, int* flags) {
+// shared memory is given back, and returns false.  Lanes poll by their own
+// clocks, so one may give up where another sees the copies land.
+__device__ __forceinline__ bool lane_wait(uint64_t* bar, int* flags) {
   if (mbar_try_wait(bar, 0)) return true;
   for (int turn = 0; turn < 2; ++turn) {
     const uint64_t start = global_timer_ns();
@@ -688,6 +690,11 @@ __device__ __forceinline__ bool bulk_wait(uint64_t* bar, int* flags) {
     atomicOr(flags, kDevErrTimeout);
   }
   return false;
+}
+
+// One answer for the warp, whose blocks need all of its lanes.
+__device__ __forceinline__ bool bulk_wait(uint64_t* bar, int* flags) {
+  return __all_sync(0xffffffffu, lane_wait(bar, flags));
 }
 
 // A block's new moments to codes and scales, by the definition.
@@ -934,7 +941,7 @@ __global__ void __launch_bounds__(ST_THREADS) state8_kernel(const Q8Chunk* __res
   const Q8Chunk ch = chunks[blockIdx.x];
   const int lane = threadIdx.x & 31, first = (threadIdx.x >> 5) * STATE8_BLOCKS * Q_BLOCK;
   pdl_wait();
-  if (first >= ch.count || halted(flags)) return;
+  if (first >= ch.count || __any_sync(0xffffffffu, halted(flags))) return;
   if (ch.second)
     ch.bf16 ? convert_run<PACK, true, true>(ch, first, lane) : convert_run<PACK, true, false>(ch, first, lane);
   else
