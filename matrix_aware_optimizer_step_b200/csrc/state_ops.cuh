@@ -823,16 +823,24 @@ __global__ void __launch_bounds__(ST_THREADS, ADAM8_CTAS)
     for (int b = whole; b * Q_BLOCK < count; ++b)
       adam8_block<PBF16, COPY, GBF16, STOCH, false>(w, mine, b, count - b * Q_BLOCK, scales, now, sc, chunks + blockIdx.x);
   }
-  if (whole > 0 && !bulk_wait(&bars[warp], flags)) return;
+  // Scales of the blocks from `from` on.  The chunk's pointers are read again:
+  // kept, they would cost the loop registers.
+  auto store_scales = [&](int from) {
+    const AdamChunk* ch = chunks + blockIdx.x;
+    const uint32_t bits = __float_as_uint(scales);
+    const float ms = moment_scale<false>(bits), rs = moment_scale<true>(bits);
+    if (lane >> 1 >= from && (lane >> 1) * Q_BLOCK < min(static_cast<int>(ch->count) - first, blocks * Q_BLOCK))
+      ((lane & 1 ? ch->v_scale : ch->m_scale) + first / Q_BLOCK)[lane >> 1] = lane & 1 ? rs : ms;
+  };
+  const bool landed = whole == 0 || bulk_wait(&bars[warp], flags);
   if (!now.go) return;
+  if (!landed) {
+    store_scales(whole);     // the tail's codes are already new
+    return;
+  }
 #pragma unroll 1
   for (int b = 0; b < whole; ++b) adam8_block<PBF16, COPY, GBF16, STOCH, true>(w, mine, b, Q_BLOCK, scales, now, sc, chunks + blockIdx.x);
-  // read again: kept, these pointers would cost the loop registers
-  const AdamChunk* ch = chunks + blockIdx.x;
-  const uint32_t bits = __float_as_uint(scales);
-  const float ms = moment_scale<false>(bits), rs = moment_scale<true>(bits);
-  if ((lane >> 1) * Q_BLOCK < min(static_cast<int>(ch->count) - first, blocks * Q_BLOCK))
-    ((lane & 1 ? ch->v_scale : ch->m_scale) + first / Q_BLOCK)[lane >> 1] = lane & 1 ? rs : ms;
+  store_scales(0);
 }
 
 // ---------------------------------------------------------------------------

@@ -44,3 +44,16 @@ def test_a_warp_takes_one_answer_from_its_wait():
 def test_a_warp_takes_one_answer_from_the_flags_and_scalars():
     assert re.search(r"d\.go = " + VOTE, body("adam_now"))
     assert re.search(VOTE + r"\s*halted\(flags\)\)", body("state8_kernel"))
+
+
+def test_a_wait_that_gives_up_leaves_no_codes_without_their_scales():
+    """Tails store their codes before the wait; their scales have to follow
+    on every way out, those of blocks that were not stepped stay."""
+    kernel = body("adamw8_kernel")
+    wait = kernel.index("bulk_wait(")
+    tail, loop = kernel.index("STOCH, false>"), kernel.index("STOCH, true>")
+    assert tail < wait < loop
+    gave_up = kernel[wait:loop]
+    at = gave_up.index("store_scales(whole)")       # ahead of the return that the failed wait takes
+    assert at < gave_up.index("return", at) and "return" not in gave_up[:at].replace("if (!now.go) return;", "")
+    assert "store_scales(0)" in kernel[loop:]
