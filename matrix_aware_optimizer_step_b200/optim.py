@@ -160,19 +160,19 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
     # -- AdamW through plans ------------------------------------------------
     def _moments(self, params, bits):
         """Zero moments where there are none; those of the other form are
-        converted."""
+        converted, and replaced when that is known to have happened."""
         convert = []
         for p in params:
             st = self.state[p]
             if "step" not in st:
-                st["step"] = 0
                 st.update(state8_zeros(p) if bits == 8 else dict(
-                    exp_avg=torch.zeros_like(p, dtype=torch.float32), exp_avg_sq=torch.zeros_like(p, dtype=torch.float32)))
+                    exp_avg=torch.zeros_like(p, dtype=torch.float32),
+                    exp_avg_sq=torch.zeros_like(p, dtype=torch.float32)), step=0)
             elif ("exp_avg_scale" in st) != (bits == 8):
                 convert.append(p)
         if not convert:
             return
-        wide, codes, scales = [], [], []
+        wide, codes, scales, converted = [], [], [], []
         for p in convert:
             st = self.state[p]
             full = {k: st[k] if bits == 8 else torch.empty_like(p, dtype=torch.float32) for k in ("exp_avg", "exp_avg_sq")}
@@ -182,12 +182,17 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
                 wide.append(full[k].contiguous())
                 codes.append(small[k])
                 scales.append(small[k + "_scale"])
-            st.pop("exp_avg_scale", None)
-            st.pop("exp_avg_sq_scale", None)
-            st.update(small if bits == 8 else full)
+            converted.append(small if bits == 8 else full)
         plan = self.ctx.state8_plan(wide, codes, scales)
         plan.pack() if bits == 8 else plan.unpack()
         plan.close()
+        # after a device-side failure the kernels have written nothing
+        self.ctx.check_device()
+        for p, new in zip(convert, converted):
+            st = self.state[p]
+            st.pop("exp_avg_scale", None)
+            st.pop("exp_avg_sq_scale", None)
+            st.update(new)
 
     def _plan(self, key, tensors, grads, build):
         """The plan of `key`, rebuilt when its tensors or the gradients' types
