@@ -193,6 +193,9 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
             st.pop("exp_avg_scale", None)
             st.pop("exp_avg_sq_scale", None)
             st.update(new)
+        # plans over the old moments would keep them allocated
+        gone = set(map(id, convert))
+        self._plans = {key: plan for key, plan in self._plans.items() if key[1] == "norm" or gone.isdisjoint(key[2])}
 
     def _plan(self, key, tensors, grads, build):
         """The plan of `key`, rebuilt when its tensors or the gradients' types

@@ -76,3 +76,27 @@ def test_a_conversion_that_the_device_skipped_raises_and_keeps_the_moments(bits)
     torch.cuda.synchronize()
     assert opt.state[p]["step"] == kept["step"] + 1 and not torch.equal(p, before)
     assert ("exp_avg_scale" in opt.state[p]) == (bits == 8)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("first,moment_bytes", [(32, 8.0), (8, 2.0 + 8 / 256)])
+def test_a_conversion_frees_the_old_moments(first, moment_bytes):
+    """32 to 8 bits gives back 8 B a parameter for 2 B and a scale for each
+    256, and back again: no plan holds what was there before."""
+    from matrix_aware_optimizer_step_b200.optim import MuonWithAuxAdam
+    n = 1 << 20
+    p = torch.nn.Parameter(torch.zeros(n, device="cuda"))
+    q = torch.nn.Parameter(torch.zeros(n, device="cuda"))
+    opt = MuonWithAuxAdam([dict(params=[p, q], use_muon=False, state_bits=first, max_grad_norm=1.0)])
+    p.grad, q.grad = torch.ones_like(p), torch.ones_like(q)
+    for both in (True, False, True):               # plans over both and over one
+        q.grad = torch.ones_like(q) if both else None
+        opt.step()
+    torch.cuda.synchronize()
+    held = torch.cuda.memory_allocated()
+    opt.param_groups[0]["state_bits"] = 40 - first
+    opt.step()
+    torch.cuda.synchronize()
+    other = 10.0 + 8 / 256 - moment_bytes
+    change = torch.cuda.memory_allocated() - held
+    assert abs(change - 2 * n * (other - moment_bytes)) <= 4096
