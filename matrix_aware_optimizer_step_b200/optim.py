@@ -31,6 +31,10 @@ MUON_DEFAULTS = dict(lr=0.02, weight_decay=0.01, momentum=0.95, nesterov=True, n
 ADAMW_DEFAULTS = dict(lr=3e-4, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.01, state_bits=32,
                       max_grad_norm=None, seed=None)
 
+# A plan that this many steps have not used is dropped: parameters whose gradients come and go ask for other plans,
+# and each holds its tensors.
+PLAN_STEPS = 16
+
 
 def _own_types(state, p):
     """A parameter's saved state on its device, copied: codes as they are,
@@ -91,7 +95,7 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
         self.ctx = MuonContext(first.device.index if device is None else device)
         self.check_every = int(check_every)
         self._steps = 0
-        self._plans = {}       # what the AdamW groups' plans were built over, and the plans
+        self._plans = {}       # what the AdamW groups' plans were built over, the plans, and the step that last used each
 
     def check(self):
         """Synchronise and raise MuonError if a device-side wait gave up since
@@ -117,6 +121,9 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
                 self._adamw_planned(i, g, params)
             else:
                 self._adamw(g, params)
+        stale = [key for key, plan in self._plans.items() if plan[3] < self._steps - PLAN_STEPS]
+        for key in stale:
+            del self._plans[key]
         self._steps += 1
         if self.check_every and self._steps % self.check_every == 0:
             self.check()
@@ -204,12 +211,11 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
         ptrs = [g.data_ptr() for g in grads]
         had = self._plans.get(key)
         if had is None or had[0] != at:
-            if len(self._plans) > 64:      # parameters that come and go
-                self._plans.clear()
-            had = self._plans[key] = [at, ptrs, build()]
+            had = self._plans[key] = [at, ptrs, build(), 0]
         elif had[1] != ptrs:
             had[2].bind_grads(grads)
             had[1] = ptrs
+        had[3] = self._steps
         had[2].forget_grads()      # a gradient freed by zero_grad is not kept to the next step
         return had[2]
 
