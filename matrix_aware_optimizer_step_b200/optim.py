@@ -19,6 +19,7 @@ library: every update runs in libmuon_b200.so.
 from __future__ import annotations
 
 from itertools import chain
+from operator import index
 from typing import Iterable
 
 import torch
@@ -34,6 +35,20 @@ ADAMW_DEFAULTS = dict(lr=3e-4, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.01, s
 # A plan that this many steps have not used is dropped: parameters whose gradients come and go ask for other plans,
 # and each holds its tensors.
 PLAN_STEPS = 16
+
+
+def _check_adamw_group(g):
+    """Refuse values of the keys beyond AdamW's own that no step can take."""
+    if g.get("state_bits", 32) not in (8, 32):
+        raise ValueError("state_bits must be 8 or 32")
+    clip, seed = g.get("max_grad_norm"), g.get("seed")
+    try:
+        if clip is not None and not clip >= 0:
+            raise ValueError("max_grad_norm must be >= 0")
+        if seed is not None and not 0 <= index(seed) < 1 << 32:
+            raise ValueError("seed must lie in [0, 2^32)")
+    except TypeError:
+        raise ValueError("max_grad_norm must be a number and seed an integer") from None
 
 
 def _own_types(state, p):
@@ -76,12 +91,7 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
             for k, v in base.items():
                 g.setdefault(k, v)
             if not g["use_muon"]:
-                if g["state_bits"] not in (8, 32):
-                    raise ValueError("state_bits must be 8 or 32")
-                if g["max_grad_norm"] is not None and not g["max_grad_norm"] >= 0:
-                    raise ValueError("max_grad_norm must be >= 0")
-                if g["seed"] is not None and not 0 <= g["seed"] < 1 << 32:
-                    raise ValueError("seed must lie in [0, 2^32)")
+                _check_adamw_group(g)
             groups.append(g)
         super().__init__(groups, dict())
         for g in self.param_groups:
@@ -108,8 +118,9 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
-        if any(g.get("state_bits", 32) not in (8, 32) for g in self.param_groups):
-            raise ValueError("state_bits must be 8 or 32")
+        for g in self.param_groups:        # all of them, before any is stepped
+            if not g.get("use_muon", True):
+                _check_adamw_group(g)
         for i, g in enumerate(self.param_groups):
             params = [p for p in g["params"] if p.grad is not None]
             if not params:
@@ -219,8 +230,9 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
         had[2].forget_grads()      # a gradient freed by zero_grad is not kept to the next step
         return had[2]
 
-    def _adamw_planned(self, index, g, params):
-        bits, clip = int(g.get("state_bits", 32)), g.get("max_grad_norm")
+    def _adamw_planned(self, group, g, params):
+        bits, clip, seed = int(g.get("state_bits", 32)), g.get("max_grad_norm"), g.get("seed")
+        seed = None if seed is None else index(seed)
         self._moments(params, bits)
         b1, b2 = g["betas"]
         hp = default_adamw_plan_hparams(lr=g["lr"], beta1=b1, beta2=b2, eps=g["eps"], weight_decay=g["weight_decay"])
@@ -228,7 +240,7 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
         factor = None
         if clip is not None:
             gs = list(grads.values())
-            norm = self._plan((index, "norm", tuple(map(id, params))), [], gs, lambda: self.ctx.grad_norm_plan(gs))
+            norm = self._plan((group, "norm", tuple(map(id, params))), [], gs, lambda: self.ctx.grad_norm_plan(gs))
             factor = norm.run(float(clip))[1:]
         by_step = {}
         for p in params:
@@ -238,9 +250,9 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
         for step, ps in by_step.items():
             lists = [[p.detach().view(-1) for p in ps]] + [[self.state[p][k].view(-1) for p in ps] for k in names]
             gs = [grads[p] for p in ps]
-            plan = self._plan((index, bits, tuple(map(id, ps))), list(chain(*lists)), gs,
+            plan = self._plan((group, bits, tuple(map(id, ps))), list(chain(*lists)), gs,
                               lambda: self.ctx.adamw_plan(lists[0], gs, *lists[1:]))
-            plan.step(step, hp, grad_scale=factor, seed=g.get("seed"))
+            plan.step(step, hp, grad_scale=factor, seed=seed)
 
     def load_state_dict(self, state_dict):
         """As torch.optim.Optimizer's, except that 8-bit codes stay what they
