@@ -244,8 +244,7 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
             factor = norm.run(float(clip))[1:]
         by_step = {}
         for p in params:
-            self.state[p]["step"] += 1
-            by_step.setdefault(self.state[p]["step"], []).append(p)
+            by_step.setdefault(self.state[p]["step"] + 1, []).append(p)
         names = ["exp_avg", "exp_avg_sq"] + (["exp_avg_scale", "exp_avg_sq_scale"] if bits == 8 else [])
         for step, ps in by_step.items():
             lists = [[p.detach().view(-1) for p in ps]] + [[self.state[p][k].view(-1) for p in ps] for k in names]
@@ -253,6 +252,8 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
             plan = self._plan((group, bits, tuple(map(id, ps))), list(chain(*lists)), gs,
                               lambda: self.ctx.adamw_plan(lists[0], gs, *lists[1:]))
             plan.step(step, hp, grad_scale=factor, seed=seed)
+            for p in ps:
+                self.state[p]["step"] = step
 
     def load_state_dict(self, state_dict):
         """As torch.optim.Optimizer's, except that 8-bit codes stay what they

@@ -92,3 +92,15 @@ def test_a_group_without_the_keys_steps(opt):
         del opt.param_groups[0][k]
     opt.step()
     assert steps(opt) == [1] * 4
+
+
+def test_a_call_that_the_library_refuses_is_not_counted(opt):
+    opt.step()
+    good = opt.param_groups[1]["lr"]
+    opt.param_groups[1]["lr"] = None
+    with pytest.raises(ValueError):
+        opt.step()
+    assert steps(opt) == [2, 2, 1, 1]
+    opt.param_groups[1]["lr"] = good
+    opt.step()
+    assert steps(opt) == [3, 3, 2, 2] and opt.ctx.calls[-1][0] == 2
