@@ -421,8 +421,9 @@ MUON_API muon_status muon_state8_unpack(muon_plan* plan, void* stream);
 
 /* No counterpart on the pages (resource management).  Free a plan of any
  * kind, waiting for work that may use it.  Graphs that captured its calls must not
- * be replayed afterwards.  Plans outlive their context only to be destroyed:
- * other calls on them then return MUON_ERR_INVALID_ARG.  NULL: no effect. */
+ * be replayed afterwards, nor once their context is destroyed.  Plans outlive
+ * their context only to be destroyed: other calls on them then return
+ * MUON_ERR_INVALID_ARG.  NULL: no effect. */
 MUON_API void muon_plan_destroy(muon_plan* plan);
 
 /* Source: "The Newton-Muon Optimizer", section "What Is Newton-Muon?" (the

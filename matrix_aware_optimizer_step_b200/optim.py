@@ -10,7 +10,13 @@ take ``lr``, ``betas``, ``eps``, ``weight_decay``.  Which parameters are
 AdamW groups take three keys more: ``state_bits`` (32, or 8 for moments in
 8 bits), ``max_grad_norm`` (clip the 2-norm over the group's gradients; a step
 whose norm is not finite changes nothing) and ``seed`` (round 8-bit codes and
-bf16 parameters stochastically).
+bf16 parameters stochastically; None, the default, rounds to nearest).
+
+A group with 8-bit moments and a beta2 near 1 needs a seed.  Rounding to
+nearest loses a change smaller than half a code: with beta2 = 0.999 a second
+moment can grow but hardly shrink, and where a block's gradients are of one
+magnitude it drifts upward (1.2 times the right value after 4000 steps, 1.8
+after 16000), which shortens the steps.
 
 This file only keeps optimizer state tensors and hands pointers to the
 library: every update runs in libmuon_b200.so.
@@ -72,8 +78,10 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
     bf16 in AdamW groups; gradients fp32 or bf16.
 
     A group's state_bits may be changed between steps, after loading a
-    checkpoint for instance: its moments are converted at the next step.
-    A step skipped for a norm that is not finite still counts.
+    checkpoint for instance: its moments are converted at the next step, which
+    synchronises the device; when that fails the old ones stay.  A step skipped
+    for a norm that is not finite still counts; one that raises does not, for
+    groups that use any of the three keys or bf16 parameters.
 
     Device-side failures (a bounded wait inside a kernel that gave up) are
     flagged on the GPU; from then on the library leaves every parameter and
