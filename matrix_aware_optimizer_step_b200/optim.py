@@ -57,18 +57,15 @@ def _check_adamw_group(g):
         raise ValueError("max_grad_norm must be a number and seed an integer") from None
 
 
-def _own_types(state, p):
-    """A parameter's saved state on its device, copied: codes as they are,
-    other tensors in fp32, the step a number."""
-    out = {}
-    for name, t in state.items():
-        if name == "step":
-            t = int(t)
-        elif isinstance(t, torch.Tensor):
-            dtype = torch.float32 if t.is_floating_point() else t.dtype
-            t = t.detach().to(device=p.device, dtype=dtype, copy=True).contiguous()
-        out[name] = t
-    return out
+def _own_types(value, p):
+    """A saved value of the state of p on its device, tensors copied: codes as
+    they are, others in fp32."""
+    if isinstance(value, torch.Tensor):
+        dtype = torch.float32 if value.is_floating_point() else value.dtype
+        return value.detach().to(device=p.device, dtype=dtype, copy=True).contiguous()
+    if isinstance(value, dict):
+        return {k: _own_types(v, p) for k, v in value.items()}
+    return type(value)(_own_types(v, p) for v in value) if isinstance(value, (list, tuple)) else value
 
 
 class MuonWithAuxAdam(torch.optim.Optimizer):
@@ -275,6 +272,9 @@ class MuonWithAuxAdam(torch.optim.Optimizer):
             saved = chain.from_iterable(g["params"] for g in sd["param_groups"])
             own = dict(zip(saved, chain.from_iterable(g["params"] for g in self.param_groups)))
             fresh.update((own[k], _own_types(st, own[k])) for k, st in sd["state"].items() if k in own)
+            for st in fresh.values():
+                if "step" in st:
+                    st["step"] = int(st["step"])
             # no tensor is left for the base class, whose cast would hold every 8-bit moment in 32 bits at once
             return dict(sd, state={k: st for k, st in sd["state"].items() if k not in own})
 

@@ -138,6 +138,22 @@ def test_tensors_never_take_the_parameters_type(make, monkeypatch):
     assert made and not [x for x in made if x[0] in (torch.int8, torch.uint8) and x[1] != x[0]]
 
 
+def test_tensors_inside_other_values_are_taken_the_same_way(make):
+    """As the base class does: what a caller keeps beside the moments, in
+    dictionaries and lists, moves and is cast like them."""
+    a, = params(1)
+    one = make([a])
+    kept = dict(ema=torch.ones(3, dtype=torch.float64), more=[torch.ones(2, dtype=torch.int8), (5, "text")])
+    one.state[a].update(step=1, mine=kept)
+    c, = params(1, torch.bfloat16)
+    two = make([c])
+    two.load_state_dict(one.state_dict())
+    mine = two.state[c]["mine"]
+    assert mine["ema"].dtype == torch.float32 and mine["more"][0].dtype == torch.int8
+    assert type(mine["more"]) is list and mine["more"][1] == (5, "text")
+    assert mine["more"][0].data_ptr() != kept["more"][0].data_ptr()
+
+
 def test_a_load_that_fails_changes_nothing(make):
     a, b = params(2)
     one = make([a, b], state_bits=8)
