@@ -30,8 +30,10 @@
 //   norm      fp32 gradients (4)                                  83   0.99
 //             bf16 gradients (2), call after call                 42   0.97
 //
-// The 8-bit step on bf16 parameters, the stochastic ones and the pack from
-// bf16 (the fp32 one's instructions on 60 % of its bytes) are bound by
+// The pack from bf16 runs the fp32 one's instructions and more (29 an element)
+// on 60 % of its bytes: 58 % of the issue slots used, and a warp that computes
+// has no loads in flight.
+// The 8-bit step on bf16 parameters and the stochastic ones are bound by
 // instruction issue, not by memory (52 to 72 instructions an element, 78 % of
 // the issue slots used, the integer pipe the busiest): two codes an element
 // cost two roots, their rounding and its check, and a hash when stochastic.
